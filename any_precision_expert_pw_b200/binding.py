@@ -45,9 +45,16 @@ EXPORTS = ("pw_block_prepare", "pw_pack_bitplanes", "pw_route_topk", "pw_topk", 
            "pw_moe_anyprec_forward",
            "pw_moe_anyprec_forward_static", "pw_set_tc_min_tokens", "pw_set_ffn_grid",
            "pw_set_wait_limit_ns", "pw_test_hold_down_items", "pw_commit_bits",
+           "pw_expert_sort_workspace_bytes", "pw_expert_sort", "pw_expert_dispatch",
+           "pw_expert_dispatch_grad", "pw_expert_combine", "pw_expert_combine_grad",
+           "pw_scaled_quantize", "pw_scaled_gemm_workspace_bytes", "pw_scaled_gemm",
+           "pw_moe_scaled_workspace_bytes", "pw_moe_scaled_forward",
            "pw_get_status",
            "pw_status_string", "pw_version")
 PW_STATIC_WORKSPACE_BYTES = 16 << 20
+PW_TYPE_F32, PW_TYPE_BF16, PW_TYPE_F16 = 0, 1, 2
+PW_MAX_ROWS = 1 << 24
+PW_MAX_COLS = 1 << 18
 
 
 class PwError(RuntimeError):
@@ -81,7 +88,15 @@ class pw_affinity_cfg(ctypes.Structure):
                 ("bin_width", ctypes.c_double)]
 
 
+class pw_scaled_experts(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("gate_up", ctypes.c_void_p),
+                ("gate_up_scale", ctypes.c_void_p), ("down", ctypes.c_void_p),
+                ("down_scale", ctypes.c_void_p)]
+
+
 assert ctypes.sizeof(pw_affinity_cfg) == 16
+assert ctypes.sizeof(pw_scaled_experts) == 48
 assert ctypes.sizeof(pw_block) == 256 and pw_block.layout.offset == 13
 assert ctypes.sizeof(pw_page_table) == 16 and ctypes.sizeof(pw_route_cfg) == 20
 
@@ -109,7 +124,6 @@ def lib() -> ctypes.CDLL:
         L.pw_affinity_remap.argtypes = [P, P, P, I, I, ctypes.POINTER(pw_route_cfg),
                                         ctypes.POINTER(pw_affinity_cfg), P, P, P, S]
         L.pw_moe_workspace_bytes.argtypes = [I, I, I, I, I]
-        L.pw_moe_workspace_bytes.restype = Z
         L.pw_moe_anyprec_forward.argtypes = [P, I, I, P, I, I, I, I, P, P, P, P, Z, S]
         L.pw_moe_anyprec_forward_static.argtypes = [P, I, I, P, I, I, I, I, P, P, P, S]
         L.pw_set_tc_min_tokens.argtypes = [I]
@@ -120,13 +134,28 @@ def lib() -> ctypes.CDLL:
         L.pw_page_copy.argtypes = [P, I, P, I, I, I, I, S]
         L.pw_page_update.argtypes = [P, I, P, I, S]
         L.pw_plan_bitwidths.argtypes = [I, P, P, P, P, ctypes.c_uint64, P]
+        LL = ctypes.c_longlong
+        L.pw_expert_sort_workspace_bytes.argtypes = [I, I, I]
+        L.pw_expert_sort.argtypes = [P, I, I, I, P, P, P, P, Z, S]
+        L.pw_expert_dispatch.argtypes = [P, I, I, I, I, LL, P, P, LL, S]
+        L.pw_expert_dispatch_grad.argtypes = [P, I, I, I, I, LL, P, P, LL, S]
+        L.pw_expert_combine.argtypes = [P, I, I, I, I, LL, P, P, P, I, LL, S]
+        L.pw_expert_combine_grad.argtypes = [P, P, I, I, I, I, LL, LL, P, P, P, LL, P, S]
+        L.pw_scaled_quantize.argtypes = [P, I, I, I, LL, I, P, LL, P, S]
+        L.pw_scaled_gemm_workspace_bytes.argtypes = [I, I, I, I]
+        L.pw_scaled_gemm.argtypes = [P, P, I, I, LL, P, P, I, I, LL, P, P, I, LL, P, Z, S]
+        L.pw_moe_scaled_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.pw_moe_scaled_forward.argtypes = [ctypes.POINTER(pw_scaled_experts), P, I, I, I, P, P, P,
+                                            I, P, Z, S]
         L.pw_get_status.argtypes = [S]
         L.pw_status_string.argtypes = [I]
         L.pw_status_string.restype = ctypes.c_char_p
         L.pw_version.restype = ctypes.c_char_p
         for name in EXPORTS:
             fn = getattr(L, name)
-            if name not in ("pw_moe_workspace_bytes", "pw_status_string", "pw_version"):
+            if name.endswith("_bytes"):
+                fn.restype = Z
+            elif name not in ("pw_status_string", "pw_version"):
                 fn.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -249,6 +278,66 @@ def pw_page_update(pt_dev, num_blocks, updates, count, stream=0) -> int:
 def pw_plan_bitwidths(nblocks, damage, bytes_, qmin, qmax, budget, q_out) -> int:
     """Host arrays as integer addresses (e.g. numpy arr.ctypes.data)."""
     return lib().pw_plan_bitwidths(nblocks, damage, bytes_, qmin, qmax, int(budget), q_out)
+
+
+def pw_expert_sort_workspace_bytes(T, k, E) -> int:
+    return int(lib().pw_expert_sort_workspace_bytes(T, k, E))
+
+
+def pw_expert_sort(idx, T, k, E, pos, src, offsets, workspace, ws_bytes, stream=0) -> int:
+    return lib().pw_expert_sort(idx, T, k, E, pos, src, offsets, workspace, ws_bytes, stream)
+
+
+def pw_expert_dispatch(x, type_, T, k, H, x_stride, pos, xs, xs_stride, stream=0) -> int:
+    return lib().pw_expert_dispatch(x, type_, T, k, H, x_stride, pos, xs, xs_stride, stream)
+
+
+def pw_expert_dispatch_grad(d_xs, type_, T, k, H, d_xs_stride, pos, d_x, d_x_stride,
+                            stream=0) -> int:
+    return lib().pw_expert_dispatch_grad(d_xs, type_, T, k, H, d_xs_stride, pos, d_x, d_x_stride,
+                                         stream)
+
+
+def pw_expert_combine(o, o_type, T, k, H, o_stride, pos, gate, y, y_type, y_stride,
+                      stream=0) -> int:
+    return lib().pw_expert_combine(o, o_type, T, k, H, o_stride, pos, gate, y, y_type, y_stride,
+                                   stream)
+
+
+def pw_expert_combine_grad(d_y, o, type_, T, k, H, d_y_stride, o_stride, pos, gate, d_o,
+                           d_o_stride, d_gate, stream=0) -> int:
+    """d_o or d_gate (not both) may be 0; o is read for d_gate only."""
+    return lib().pw_expert_combine_grad(d_y, o, type_, T, k, H, d_y_stride, o_stride, pos, gate,
+                                        d_o, d_o_stride, d_gate, stream)
+
+
+def pw_scaled_quantize(x, type_, rows, cols, x_stride, block_rows, q, q_stride, scale,
+                       stream=0) -> int:
+    """block_rows: 1 (activations) or 128 (weights)."""
+    return lib().pw_scaled_quantize(x, type_, rows, cols, x_stride, block_rows, q, q_stride, scale,
+                                    stream)
+
+
+def pw_scaled_gemm_workspace_bytes(M, N, K, E) -> int:
+    return int(lib().pw_scaled_gemm_workspace_bytes(M, N, K, E))
+
+
+def pw_scaled_gemm(x_q, x_scale, M, K, x_stride, w_q, w_scale, E, N, w_stride, offsets, y, y_type,
+                   y_stride, workspace, ws_bytes, stream=0) -> int:
+    """offsets: device int32[E + 1], or 0 with E = 1."""
+    return lib().pw_scaled_gemm(x_q, x_scale, M, K, x_stride, w_q, w_scale, E, N, w_stride,
+                                offsets, y, y_type, y_stride, workspace, ws_bytes, stream)
+
+
+def pw_moe_scaled_workspace_bytes(T, k, E, H, I) -> int:
+    return int(lib().pw_moe_scaled_workspace_bytes(T, k, E, H, I))
+
+
+def pw_moe_scaled_forward(experts, x, x_type, T, k, idx, gate, y, y_type, workspace, ws_bytes,
+                          stream=0) -> int:
+    """experts: a pw_scaled_experts (host struct of device pointers)."""
+    return lib().pw_moe_scaled_forward(_cfg(experts), x, x_type, T, k, idx, gate, y, y_type,
+                                       workspace, ws_bytes, stream)
 
 
 class pw_page_update_t(ctypes.Structure):

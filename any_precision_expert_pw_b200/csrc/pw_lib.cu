@@ -19,6 +19,8 @@
 #include "pw_group.cuh"
 #include "pw_pack.cuh"
 #include "pw_route.cuh"
+#include "pw_rows.cuh"
+#include "pw_scaled.cuh"
 #include "pw_table.cuh"
 #include "pw_tc.cuh"
 
@@ -30,6 +32,7 @@ static_assert(sizeof(pw_page_table) == 16, "pw_page_table layout");
 static_assert(sizeof(pw_route_cfg) == 20, "pw_route_cfg layout");
 static_assert(sizeof(pw_affinity_cfg) == 16, "pw_affinity_cfg layout");
 static_assert(sizeof(pw_page_update_t) == 16, "pw_page_update_t layout");
+static_assert(sizeof(pw_scaled_experts) == 48, "pw_scaled_experts layout");
 static_assert(offsetof(pw_block, stored_bits) == 14, "pw_block layout");
 
 namespace {
@@ -501,6 +504,8 @@ pw_status pw_get_status(pw_stream_t stream) {
 }  // extern "C"
 
 // Routing-side entry points (pw_route_topk, pw_topk, pw_substitute, pw_remap, AffinityBinning,
-// the expert cache) and page movement / planning: same translation unit.
+// the expert cache), page movement / planning, and the expert-row and scaled-product calls: same
+// translation unit.
 #include "pw_route_api.cuh"
 #include "pw_page_api.cuh"
+#include "pw_rows_api.cuh"

@@ -1,0 +1,531 @@
+// K7: products in 8-bit floating point (e4m3) with fp32 scales, one per activation row and 128
+// columns and one per 128 x 128 block of a weight matrix, dense or grouped by expert:
+//
+//   y[r][n] = sum_b sx[r][b] sw[e(r)][n / 128][b] * P_b,   P_b = sum_{c in block b} xq[r][c] wq[e][n][c]
+//
+// Every P_b is formed by the tensor cores (tcgen05, kind::f8f6f4: products exact, sums fp32 in tensor
+// memory) over the block's 128 columns; scales are general fp32 numbers, so P_b is then read back
+// and folded into fp32 registers with one fused multiply-add per element and block.  The gated form
+// multiplies a gate and an up half, and its epilogue forms h = SiLU(gate) * up and quantises it for
+// the next product (one power-of-two scale per row and 128 features: one tile).
+//
+// Work: units of 128 rows x 256 columns (gated: 128 gate and the 128 matching up columns), in order
+// of expert, column tile, row tile; one CTA per SM.  Whole waves of units go one unit to a CTA.  The
+// rest (U mod SMs units) is cut along K into equal runs of K blocks, one per CTA, so a decode step
+// with few units still streams weights on every SM; a unit cut into pieces is joined by the CTA that
+// finishes last (partials and a counter in the workspace; the sum runs in piece order whoever joins,
+// so results repeat bit for bit).  Nobody waits for another CTA.
+//
+// Warps: 0 TMA producer (4 stages of 16 KB rows + 32 KB weights; few rows: only their 16-row boxes),
+// 1 MMA issuer (4 MMAs of 128 x 256 x 32 a block into one of two tensor-memory stages), 2 tensor
+// memory, 4-11 epilogue (two warps per 32-row quarter, 128 columns each; warps whose rows are all
+// beyond the group only keep the barriers).
+#pragma once
+#include <cuda.h>
+
+#include "pw_common.cuh"
+#include "pw_ffn.cuh"
+#include "pw_rows.cuh"
+#include "pw_tc.cuh"
+
+namespace pw {
+namespace k7 {
+
+constexpr int kTileM = 128, kTileN = 256, kBlk = 128;
+constexpr int kStages = 4;
+constexpr int kABytes = kTileM * kBlk, kBBytes = kTileN * kBlk;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kSmallRows = 16;  // rows of the small activation box
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 256;
+// registers a thread: 40 in the producer warpgroup, 232 in the two epilogue warpgroups (128
+// accumulators and two buffers of 32); their sum may not exceed what the block is launched with
+constexpr int kProducerRegs = 40, kEpilogueRegs = 232;
+constexpr int kSplitRegs = 128 * kProducerRegs + kEpiThreads * kEpilogueRegs;
+static_assert(kSplitRegs <= 65536, "register file");
+constexpr int kTmemCols = 512, kAccCols = 256;
+constexpr int kMinPiece = 4;  // K blocks: shorter pieces cost more in joining than they spread
+
+constexpr int kOffBar = kStages * kStageBytes;
+constexpr int kNumBars = 2 * kStages + 4 + 1;
+constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) / 16) * 16;
+constexpr int kOffAmax = kOffMisc + 32;
+constexpr int kOffTiles = kOffAmax + 2 * kTileM * 4;  // [E + 1] row tiles before each expert
+constexpr int smem_bytes(int E) { return kOffTiles + 2 * (E + 1) * 4; }
+static_assert(smem_bytes(PW_MAX_EXPERTS) <= 227 * 1024, "shared memory budget");
+
+struct alignas(64) Params {
+  CUtensorMap xmap;    // rows, box 128 columns x 128 rows
+  CUtensorMap xsmall;  // rows, box 128 columns x 16 rows
+  CUtensorMap wmap;    // weights [E][N][K], box 128 columns x 256 rows (gated: 64)
+  const float* sx;
+  const float* sw;
+  const int32_t* offsets;  // [E + 1] or NULL: one expert, all M rows
+  int M, N, K, E;
+  int kb, nb, nt;  // K blocks, N scale blocks, column tiles
+  void* y;
+  size_t ld_y;
+  int vec;  // rows of y may be stored 16 bytes at a time
+  uint8_t* hq;  // gated: e4m3 [M][I], fp32 scales [M][I / 128]
+  float* hs;
+  int I;
+  float* part;       // [2 per CTA][256][rcap]
+  int rcap;
+  int32_t* counter;  // [CTAs], zero at launch
+};
+
+// ---- schedule (the same in every role) ----
+struct Sched {
+  int units, waves, rem, pieces, run;  // run: K blocks of the remainder, cut into `pieces`
+};
+__device__ __forceinline__ Sched make_sched(int units, int kb, int grid) {
+  Sched s;
+  s.units = units;
+  s.waves = units / grid;
+  s.rem = units - s.waves * grid;
+  s.run = s.rem * kb;
+  s.pieces = min(grid, max(s.rem, s.run / kMinPiece));
+  return s;
+}
+__device__ __forceinline__ int piece_begin(const Sched& s, int p) {
+  return static_cast<int>(static_cast<long long>(s.run) * p / s.pieces);
+}
+__device__ __forceinline__ int piece_of(const Sched& s, int x) {  // the piece that holds K block x
+  return static_cast<int>((static_cast<long long>(x + 1) * s.pieces - 1) / s.run);
+}
+struct Piece {
+  int unit, k0, k1;
+  int first, count, slot;  // pieces of the unit, and this one's workspace slot
+};
+// The i-th piece of a CTA.  A piece of the remainder is at most one unit long (pieces >= rem), so
+// it touches at most two units.
+__device__ __forceinline__ bool get_piece(const Sched& s, int kb, int i, Piece& p) {
+  const int cta = blockIdx.x;
+  p.first = 0;
+  p.count = 1;
+  p.slot = 0;
+  if (i < s.waves) {
+    p.unit = cta + i * static_cast<int>(gridDim.x);
+    p.k0 = 0;
+    p.k1 = kb;
+    return true;
+  }
+  if (s.rem == 0 || cta >= s.pieces) return false;
+  int a = piece_begin(s, cta);
+  const int b = piece_begin(s, cta + 1);
+  const int j0 = a / kb;
+  if (i > s.waves) {
+    if (i > s.waves + 1) return false;
+    a = (j0 + 1) * kb;
+  }
+  if (a >= b) return false;
+  const int j = a / kb;
+  p.unit = s.waves * static_cast<int>(gridDim.x) + j;
+  p.k0 = a - j * kb;
+  p.k1 = min(kb, p.k0 + b - a);
+  p.first = piece_of(s, j * kb);
+  p.count = piece_of(s, (j + 1) * kb - 1) - p.first + 1;
+  p.slot = 2 * cta + (i > s.waves ? 1 : 0);
+  return true;
+}
+
+struct Unit {
+  int e, row0, rows, n;  // expert, first row, rows (<= 128), column tile
+};
+__device__ __forceinline__ Unit find_unit(const Params& p, const int* tiles, const int* first, int u) {
+  const int v = u / p.nt;
+  int lo = 0, hi = p.E - 1;  // the last expert with tiles[e] <= v that has tiles
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tiles[mid] <= v) lo = mid;
+    else hi = mid - 1;
+  }
+  Unit r;
+  r.e = lo;
+  const int mt = tiles[lo + 1] - tiles[lo];
+  const int local = u - p.nt * tiles[lo];
+  r.n = local / mt;
+  const int m = local - r.n * mt;
+  r.row0 = first[lo] + m * kTileM;
+  r.rows = min(kTileM, first[lo + 1] - r.row0);
+  return r;
+}
+
+// ---- tcgen05 / TMA ----
+// Shared-memory descriptor of a K-major operand with 128-byte swizzle (8 rows x 128 bytes atoms,
+// 1024 bytes apart).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+// kind::f8f6f4, e4m3 x e4m3 (both K-major) -> fp32, M = 128, N = 256.
+constexpr uint32_t kInstr = (1u << 4) | ((kTileN >> 3) << 17) | ((kTileM >> 4) << 24);
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(kInstr), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// 32 columns of this warp's lane quarter, asynchronously; the registers hold them after tmem_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// The registers pass through the wait so that nothing that uses them moves above it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void fold32(float* acc, const uint32_t (&r)[32], float s) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
+}
+
+// SiLU(g) * u.  The hardware exponential and reciprocal (errors of a few 2^-22) are far below the
+// 2^-4 step of the e4m3 value that h becomes.
+__device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// 128 columns of one row (a thread): stores of 16 bytes where alignment and the edge allow.
+template <int TY>
+__device__ __forceinline__ void store_row(void* y, size_t at, int n, int N, int vec, const float (&acc)[128]) {
+  constexpr int S = ElemSize<TY>::value;
+  if (vec && n + 128 <= N) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
+      store_elems<TY, 8>(elem_at(y, at + n + c, S), v);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 128; ++c)
+      if (n + c < N) {
+        const float v[1] = {acc[c]};
+        store_elems<TY, 1>(elem_at(y, at + n + c, S), v);
+      }
+  }
+}
+
+// GATED: the gate_up product (N = 2I; I % 128 == 0).  TO: type of y (GATED: unused).
+template <bool GATED, int TO>
+__global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_constant__ Params p) {
+  uint8_t* const smem = k4::g_smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_last = reinterpret_cast<int*>(tmem_slot + 2);
+  float* s_amax = reinterpret_cast<float*>(smem + kOffAmax);
+  int* s_tiles = reinterpret_cast<int*>(smem + kOffTiles);  // [E + 1]
+  const int E = p.E;
+  int* s_first = s_tiles + E + 1;                           // [E + 1] offsets
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (smem_u32(smem) & 1023) {  // the swizzled buffers start on 1024-byte boundaries
+    if (threadIdx.x == 0) set_status(PW_ERR_UNSUPPORTED);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kEpiThreads / 32);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    prefetch_map(&p.xmap);
+    prefetch_map(&p.xsmall);
+    prefetch_map(&p.wmap);
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  griddep_wait();
+  griddep_launch();
+  // row tiles before each expert; offsets that decrease or leave [0, M] give no rows
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    const int o = p.offsets ? p.offsets[e] : (e ? p.M : 0);
+    s_first[e] = min(max(o, 0), p.M);
+    if (o < 0 || o > p.M) set_status(PW_ERR_BOUNDS);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      int v = 0;
+      if (e < E) {
+        const int rows = s_first[e + 1] - s_first[e];
+        if (rows < 0 && blockIdx.x == 0) set_status(PW_ERR_BOUNDS);
+        v = rows > 0 ? (rows + kTileM - 1) / kTileM : 0;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+      }
+      if (e < E) s_tiles[e + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) s_tiles[0] = 0;
+  }
+  k5::tc_fence_before();
+  __syncthreads();
+  k5::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Sched sched = make_sched(s_tiles[E] * p.nt, p.kb, gridDim.x);
+  const uint32_t smem_base = smem_u32(smem);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if (warp == 0 && lane == 0) {
+      // ---------------- producer ----------------
+      uint32_t g = 0;
+      Piece pc;
+      bool ok = true;
+      for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
+        const Unit u = find_unit(p, s_tiles, s_first, pc.unit);
+        const bool whole = u.rows > kTileM / 2;
+        const int boxes = (u.rows + kSmallRows - 1) / kSmallRows;
+        const uint32_t bytes = kBBytes + (whole ? kABytes : boxes * kSmallRows * kBlk);
+        for (int b = pc.k0; b < pc.k1; ++b, ++g) {
+          const int s = g % kStages;
+          if (!(ok = k5::wait_bar(&empty[s], ((g / kStages) & 1) ^ 1, abort_flag))) break;
+          mbar_arrive_expect_tx(&full[s], bytes);
+          const uint32_t a = smem_base + s * kStageBytes, w = a + kABytes;
+          if (GATED) {  // 64 gate, 64 up, 64 gate, 64 up rows: each epilogue half has both
+            for (int q = 0; q < 4; ++q)
+              tma_3d(w + q * (kBBytes / 4), &p.wmap, b * kBlk,
+                     (q & 1 ? p.I : 0) + u.n * 128 + (q >> 1) * 64, u.e, &full[s]);
+          } else {
+            tma_3d(w, &p.wmap, b * kBlk, u.n * kTileN, u.e, &full[s]);
+          }
+          if (whole) {
+            tma_2d(a, &p.xmap, b * kBlk, u.row0, &full[s]);
+          } else {
+            for (int q = 0; q < boxes; ++q)
+              tma_2d(a + q * kSmallRows * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kSmallRows, &full[s]);
+          }
+        }
+      }
+      // every issued copy has landed before the block exits
+      for (uint32_t x = (g > kStages ? g - kStages : 0); x < g; ++x)
+        mbar_wait(&full[x % kStages], (x / kStages) & 1);
+    } else if (warp == 1 && lane == 0) {
+      // ---------------- MMA issuer ----------------
+      uint32_t g = 0;
+      Piece pc;
+      bool ok = true;
+      for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
+        for (int b = pc.k0; b < pc.k1; ++b, ++g) {
+          const int s = g % kStages, t = g & 1;
+          if (!(ok = k5::wait_bar(&acc_empty[t], ((g >> 1) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = k5::wait_bar(&full[s], (g / kStages) & 1, abort_flag))) break;
+          k5::tc_fence_after();
+          const uint64_t ad = sw128_desc(smem_base + s * kStageBytes);
+          const uint64_t bd = sw128_desc(smem_base + s * kStageBytes + kABytes);
+          const uint32_t d = tmem_base + t * kAccCols;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_f8(d, ad + 2 * j, bd + 2 * j, j > 0);  // 32 bytes of K each
+          k5::mma_commit(&empty[s]);
+          k5::mma_commit(&acc_full[t]);
+        }
+      }
+      k5::mma_commit(mma_done);
+      mbar_wait(mma_done, 0);
+    }
+  } else {
+    // ---------------- epilogue ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+    const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+    uint32_t g = 0;
+    Piece pc;
+    bool dead = false;  // a wait gave up: keep every barrier, write zeros
+    for (int i = 0; get_piece(sched, p.kb, i, pc); ++i) {
+      const Unit u = find_unit(p, s_tiles, s_first, pc.unit);
+      const bool mine = quarter * 32 < u.rows;  // the warp has rows
+      const bool live = r < u.rows;
+      const size_t row = static_cast<size_t>(u.row0) + (live ? r : u.rows - 1);
+      const float* sx = p.sx + row * p.kb;
+      int n0 = GATED ? u.n : 2 * u.n + half;  // 128-row scale block of columns 0-63 of the half
+      int n1 = GATED ? p.I / 128 + u.n : n0;  // and of columns 64-127
+      n0 = min(n0, p.nb - 1);
+      n1 = min(n1, p.nb - 1);
+      const float* sw0 = p.sw + (static_cast<size_t>(u.e) * p.nb + n0) * p.kb;
+      const float* sw1 = p.sw + (static_cast<size_t>(u.e) * p.nb + n1) * p.kb;
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      float a_next = __ldg(sx + pc.k0), w0_next = __ldg(sw0 + pc.k0), w1_next = GATED ? __ldg(sw1 + pc.k0) : 0.0f;
+      for (int b = pc.k0; b < pc.k1; ++b, ++g) {
+        const int t = g & 1;
+        const float s0 = a_next * w0_next, s1 = GATED ? a_next * w1_next : s0;
+        if (b + 1 < pc.k1) {
+          a_next = __ldg(sx + b + 1);
+          w0_next = __ldg(sw0 + b + 1);
+          if (GATED) w1_next = __ldg(sw1 + b + 1);
+        }
+        if (!__all_sync(0xffffffffu, k5::wait_bar(&acc_full[t], (g >> 1) & 1, abort_flag))) {
+          dead = true;
+        } else {
+          k5::tc_fence_after();
+          if (mine) {
+            uint32_t v0[32], v1[32];
+            const uint32_t ta = lane_addr + t * kAccCols;
+            tmem_ld32(ta, v0);
+            tmem_wait(v0);
+            tmem_ld32(ta + 32, v1);
+            fold32(acc, v0, s0);
+            tmem_wait(v1);
+            tmem_ld32(ta + 64, v0);
+            fold32(acc + 32, v1, s0);
+            tmem_wait(v0);
+            tmem_ld32(ta + 96, v1);
+            fold32(acc + 64, v0, s1);
+            tmem_wait(v1);
+            k5::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[t]);
+            fold32(acc + 96, v1, s1);
+            continue;
+          }
+        }
+        k5::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[t]);
+      }
+      if (dead) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      }
+      if (pc.count > 1) {
+        // partial tile to the workspace; the last piece to arrive adds all of them in piece order
+        const size_t slot_floats = static_cast<size_t>(kTileN) * p.rcap;
+        if (live) {
+          float* d = p.part + pc.slot * slot_floats + static_cast<size_t>(half * 128) * p.rcap + r;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) __stcg(d + static_cast<size_t>(c) * p.rcap, acc[c]);
+        }
+        __threadfence();
+        named_sync(1, kEpiThreads);
+        if (threadIdx.x == 128)
+          *s_last = atomicAdd(p.counter + (pc.unit - sched.waves * static_cast<int>(gridDim.x)), 1) ==
+                    pc.count - 1;
+        named_sync(1, kEpiThreads);
+        if (!*s_last) continue;
+        __threadfence();
+        if (live) {
+          const int j = pc.unit - sched.waves * static_cast<int>(gridDim.x);
+#pragma unroll
+          for (int c0 = 0; c0 < 128; c0 += 16) {
+            float v[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = 0.0f;
+            for (int q = pc.first; q < pc.first + pc.count; ++q) {
+              const int slot = 2 * q + (piece_begin(sched, q) / p.kb == j ? 0 : 1);
+              const float* d = p.part + slot * slot_floats + static_cast<size_t>(half * 128 + c0) * p.rcap + r;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) v[c] += __ldcg(d + static_cast<size_t>(c) * p.rcap);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[c0 + c] = v[c];
+          }
+        }
+      }
+      if constexpr (GATED) {
+        float m = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          acc[c] = gated(acc[c], acc[64 + c]);
+          m = fmaxf(m, finite_abs(acc[c]));
+        }
+        named_sync(1, kEpiThreads);  // the previous tile's maxima are read
+        s_amax[half * kTileM + r] = m;
+        named_sync(1, kEpiThreads);
+        m = fmaxf(s_amax[r], s_amax[kTileM + r]);
+        const int ex = scale_exponent(m);
+        const float inv = pow2(-ex);
+        if (live) {
+          if (half == 0) p.hs[row * (p.I / 128) + u.n] = pow2(ex);
+          uint4* d = reinterpret_cast<uint4*>(p.hq + row * p.I + u.n * 128 + half * 64);
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = e4m3_pair(acc[c + 4 * q] * inv, acc[c + 4 * q + 1] * inv) |
+                     (e4m3_pair(acc[c + 4 * q + 2] * inv, acc[c + 4 * q + 3] * inv) << 16);
+            d[c / 16] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else if (live) {
+        store_row<TO>(p.y, row * p.ld_y, u.n * kTileN + half * 128, p.N, p.vec, acc);
+      }
+    }
+  }
+
+  k5::tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    k5::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+}  // namespace k7
+}  // namespace pw

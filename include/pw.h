@@ -431,6 +431,130 @@ pw_status pw_plan_bitwidths(int nblocks, const double* damage, const uint64_t* b
                             const uint8_t* qmin, const uint8_t* qmax, uint64_t budget,
                             uint8_t* q_out);
 
+/* =======================================================================================
+ * Token rows sorted by expert and back, and products in 8-bit floating point.
+ *
+ * The calls below take batches of any length (a prompt, a training batch) and the routing that
+ * pw_route_topk and the rewrites give.  idx[t][s] = -1 is an empty slot (a padded token, a
+ * dropped assignment): it has no row, adds nothing to a sum and gets a zero gradient.  Rows
+ * behind the last one in use (offsets[E]) are neither read nor written.
+ * Row strides are in elements.  Sums are fp32 and each output is rounded once, to nearest even.
+ * Every sum has a fixed order: results repeat bit for bit.
+ * Row pointers are aligned to their elements; 16-byte aligned rows of whole 16-byte vectors are
+ * moved 16 bytes at a time.  Outputs may not overlap inputs.
+ * ===================================================================================== */
+
+/* Element types of the row calls. */
+enum { PW_TYPE_F32 = 0, PW_TYPE_BF16 = 1, PW_TYPE_F16 = 2 };
+
+#define PW_MAX_ROWS (1 << 24) /* T * k of a row call, rows of a quantisation or a product */
+#define PW_MAX_COLS (1 << 18) /* columns and row strides                                  */
+
+/* ---------------------------------------------------------------------------------------
+ * pw_expert_sort [LX1]: the slots of a batch sorted by expert, stable (ascending slot t*k + s
+ * within an expert).
+ *   idx [T][k] int32 in [0, E) or -1; another value records PW_ERR_BAD_EXPERT and counts as -1.
+ *   pos [T][k]: row of each slot (-1: empty).  src [T*k]: slot behind each row; entries from
+ *   offsets[E] on are left as they were.  offsets [E+1]: rows of expert e are
+ *   offsets[e] .. offsets[e+1] - 1.
+ *   1 <= k <= PW_MAX_TOPK, 1 <= T * k <= PW_MAX_ROWS, 1 <= E <= PW_MAX_EXPERTS.
+ *   workspace: >= pw_expert_sort_workspace_bytes(T, k, E) bytes (0 on bad sizes), 256-byte
+ *   aligned, contents need no initialisation.
+ * ------------------------------------------------------------------------------------- */
+size_t pw_expert_sort_workspace_bytes(int T, int k, int E);
+pw_status pw_expert_sort(const int32_t* idx, int T, int k, int E, int32_t* pos, int32_t* src,
+                         int32_t* offsets, void* workspace, size_t ws_bytes, pw_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * pw_expert_dispatch: xs[pos[t][s]] = x[t] for every slot in use (x [T][H], xs [T*k][H], both
+ *   of `type`).  pw_expert_dispatch_grad: its gradient, d_x[t] = sum over s of
+ *   d_xs[pos[t][s]] in slot order (a token without slots gets zeros).
+ *   pos as pw_expert_sort writes it: a row occurs once; a value outside [-1, T*k) records
+ *   PW_ERR_BOUNDS and its slot is skipped.  1 <= H <= stride <= PW_MAX_COLS.
+ * ------------------------------------------------------------------------------------- */
+pw_status pw_expert_dispatch(const void* x, int type, int T, int k, int H, long long x_stride,
+                             const int32_t* pos, void* xs, long long xs_stride, pw_stream_t stream);
+pw_status pw_expert_dispatch_grad(const void* d_xs, int type, int T, int k, int H,
+                                  long long d_xs_stride, const int32_t* pos, void* d_x,
+                                  long long d_x_stride, pw_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * pw_expert_combine: y[t] = sum over s, in slot order, of gate[t][s] * o[pos[t][s]]
+ *   (o [T*k][H] of o_type, gate [T][k] fp32, y [T][H] of y_type; the types may differ).
+ * pw_expert_combine_grad: its gradients for d_y [T][H] (d_y, o and d_o of one type):
+ *   d_o[pos[t][s]] = gate[t][s] * d_y[t];  d_gate[t][s] = <d_y[t], o[pos[t][s]]> (fp32; 0 for an
+ *   empty slot).  Either output may be NULL, not both; o is read for d_gate only.
+ * ------------------------------------------------------------------------------------- */
+pw_status pw_expert_combine(const void* o, int o_type, int T, int k, int H, long long o_stride,
+                            const int32_t* pos, const float* gate, void* y, int y_type,
+                            long long y_stride, pw_stream_t stream);
+pw_status pw_expert_combine_grad(const void* d_y, const void* o, int type, int T, int k, int H,
+                                 long long d_y_stride, long long o_stride, const int32_t* pos,
+                                 const float* gate, void* d_o, long long d_o_stride, float* d_gate,
+                                 pw_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * pw_scaled_quantize: x [rows][cols] to e4m3 with one fp32 scale per block of block_rows rows
+ *   (1: activations; 128: weights) and 128 columns: q * scale stands for x.
+ *   The scale is the smallest power of two 2^e, e >= -126, with |x| <= 448 * 2^e over the
+ *   block's finite values (1 if they are all zero), so x / scale is exact and q is its nearest
+ *   e4m3 value (ties to even).  Infinities and NaN become the e4m3 NaN.
+ *   q [rows][q_stride] bytes: 16-byte aligned, q_stride a multiple of 16; bytes behind column
+ *   cols are left as they were.  scale [ceil(rows / block_rows)][ceil(cols / 128)].
+ * ------------------------------------------------------------------------------------- */
+pw_status pw_scaled_quantize(const void* x, int type, int rows, int cols, long long x_stride,
+                             int block_rows, uint8_t* q, long long q_stride, float* scale,
+                             pw_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * pw_scaled_gemm: y = x W^T with both operands in e4m3, one matrix or one per expert:
+ *   y[r][n] = sum over blocks b of x_scale[r][b] * w_scale[e][n / 128][b] *
+ *             sum over the 128 columns c of b of x_q[r][c] * w_q[e][n][c],
+ *   e the expert with offsets[e] <= r < offsets[e + 1].  Scales are any fp32 numbers.
+ *   x_q [M][x_stride], w_q [E][N][w_stride] e4m3 bytes (16-byte aligned, strides multiples of
+ *   16, K of each row used), x_scale [M][ceil(K / 128)],
+ *   w_scale [E][ceil(N / 128)][ceil(K / 128)], offsets [E + 1] int32 on the device as
+ *   pw_expert_sort writes them (NULL with E = 1: all M rows), y [M][y_stride] of y_type.
+ *   An expert may have no rows.  Offsets that decrease or leave [0, M] record PW_ERR_BOUNDS,
+ *   and the rows they do not give are left as they were.
+ *   1 <= M <= PW_MAX_ROWS; 1 <= N, K, strides <= PW_MAX_COLS.  A square block transposes
+ *   with its scale, so the gradient d_x = d_y W is this call on W^T (K and N exchanged).
+ *   workspace: >= pw_scaled_gemm_workspace_bytes(M, N, K, E) bytes (0 on bad sizes), 256-byte
+ *   aligned, contents need no initialisation; calls that may overlap need one each.
+ * ------------------------------------------------------------------------------------- */
+size_t pw_scaled_gemm_workspace_bytes(int M, int N, int K, int E);
+pw_status pw_scaled_gemm(const uint8_t* x_q, const float* x_scale, int M, int K,
+                         long long x_stride, const uint8_t* w_q, const float* w_scale, int E,
+                         int N, long long w_stride, const int32_t* offsets, void* y, int y_type,
+                         long long y_stride, void* workspace, size_t ws_bytes,
+                         pw_stream_t stream);
+
+/* Experts of one layer in e4m3 with a scale per 128 x 128 block: gate_up [E][2I][H] (gate rows
+ * 0..I-1, up rows I..2I-1), its scales [E][2I/128][H/128], down [E][H][I], scales
+ * [E][H/128][I/128].  The struct is read on the host; its pointers are device pointers. */
+typedef struct pw_scaled_experts {
+  int32_t E, H, I, reserved;
+  const uint8_t* gate_up;
+  const float* gate_up_scale;
+  const uint8_t* down;
+  const float* down_scale;
+} pw_scaled_experts;
+
+/* ---------------------------------------------------------------------------------------
+ * pw_moe_scaled_forward: the expert FFN of pw_moe_anyprec_forward on e4m3 experts:
+ *   xq = quantised x (a scale per row and 128 columns), g = W_gate xq, u = W_up xq,
+ *   h = SiLU(g) * u in fp32, quantised the same way, o = W_down h (fp32),
+ *   y[t] = sum over s, in slot order, of gate[t][s] * o.
+ *   x [T][H] of x_type, idx [T][k] as in pw_expert_sort, gate [T][k] fp32, y [T][H] of y_type.
+ *   H % 128 == 0, I % 128 == 0, T * k <= PW_MAX_ROWS (T is not bound by PW_MAX_TOKENS).
+ *   workspace: >= pw_moe_scaled_workspace_bytes(T, k, E, H, I) bytes (0 on bad sizes), 256-byte
+ *   aligned, contents need no initialisation; calls that may overlap need one each.
+ * ------------------------------------------------------------------------------------- */
+size_t pw_moe_scaled_workspace_bytes(int T, int k, int E, int H, int I);
+pw_status pw_moe_scaled_forward(const pw_scaled_experts* experts, const void* x, int x_type, int T,
+                                int k, const int32_t* idx, const float* gate, void* y, int y_type,
+                                void* workspace, size_t ws_bytes, pw_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------
  * pw_get_status: synchronises `stream`, then returns and clears the device status word of
  * the current device (PW_OK if no device-side error was recorded).  Not capturable.

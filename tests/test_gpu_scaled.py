@@ -1,0 +1,335 @@
+"""Quantisation to e4m3 and products on it, against the float64 oracle (bounds: scaled_helpers)."""
+import numpy as np
+import pytest
+
+from any_precision_expert_pw_b200 import binding as B
+from any_precision_expert_pw_b200.inputs import CONFIGS
+from oracle import scaled as S
+from scaled_helpers import U, moe_bound, padded_codes, sum_bound, weights
+from test_gpu_rows import TYPES, Strided, _torch_type, gpu, half_step, routing
+
+pytestmark = pytest.mark.gpu
+
+QUANT = [(1, 1, 0, 0), (3, 128, 0, 0), (5, 100, 28, 0), (130, 257, 3, 1), (64, 384, 0, 0), (200, 1000, 8, 8)]
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("rows,cols,extra,base", QUANT)
+def test_quantize(libpw, rows, cols, extra, base, name, block_rows):
+    import torch
+    rng = np.random.default_rng([rows, cols, block_rows])
+    v = rng.normal(size=(rows, cols)) * np.exp(rng.normal(size=(rows, 1)) * 3)
+    v[0, 0] = 0.0
+    v[rows // 2] = 0.0                                     # blocks of zeros
+    if rows > 2:
+        v[2, cols // 2] = np.inf
+        v[2, 0] = np.nan
+        v[1] *= 2.0 ** -20 if name == "f16" else 2.0 ** -130  # subnormal values
+    x = Strided(rows, cols, name, extra, base, gpu(v))
+    ld = -(-cols // 16) * 16 + 16
+    q = torch.full((rows, ld), 0x5A, dtype=torch.uint8, device="cuda")
+    scale = torch.full((-(-rows // block_rows), -(-cols // 128)), -7.0, device="cuda")
+    B.check(B.pw_scaled_quantize(x.ptr, TYPES[name], rows, cols, x.ld, block_rows, q.data_ptr(), ld,
+                                 scale.data_ptr()))
+    want_q, want_s = S.quantize(x.np(), block_rows)
+    assert np.array_equal(scale.double().cpu().numpy(), want_s)
+    got = q.cpu().numpy()
+    assert (got[:, cols:] == 0x5A).all()                   # behind the columns: left as they were
+    a, b = S.TABLE[got[:, :cols]], S.TABLE[want_q]
+    assert np.array_equal(np.isnan(a), np.isnan(b))
+    assert np.array_equal(a[~np.isnan(a)], b[~np.isnan(b)])
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+def test_quantize_borders(libpw, name):
+    """Every e4m3 value and every border between two, both signs, and the scale's own borders."""
+    import torch
+    vals = np.concatenate([S._POS, (S._POS[:-1] + S._POS[1:]) / 2])
+    vals = np.concatenate([vals, -vals])
+    rows = []
+    for e in (-8, 0, 5):
+        for lead in (448.0, 449.0 if name != "bf16" else 450.0, 447.0 if name != "bf16" else 446.0):
+            for i in range(0, len(vals), 127):
+                r = np.zeros(128)
+                c = vals[i:i + 127]
+                r[:len(c)] = c
+                r[127] = lead
+                rows.append(r * 2.0 ** e)
+    x = gpu(np.array(rows)).to(_torch_type(name))
+    q = torch.empty(len(rows), 128, dtype=torch.uint8, device="cuda")
+    s = torch.empty(len(rows), 1, device="cuda")
+    B.check(B.pw_scaled_quantize(x.data_ptr(), TYPES[name], len(rows), 128, 128, 1, q.data_ptr(), 128,
+                                 s.data_ptr()))
+    want_q, want_s = S.quantize(x.double().cpu().numpy(), 1)
+    assert np.array_equal(s.double().cpu().numpy(), want_s)
+    assert np.array_equal(S.TABLE[q.cpu().numpy()], S.TABLE[want_q])
+
+
+def product(x_np, q, s, off, N, y_name, extra=0, base=0, x_extra=0, w_extra=0, poison=0xFF):
+    """Quantise x and multiply; returns (y Strided, quantised values of x)."""
+    import torch
+    M, K = x_np.shape
+    E = q.shape[0]
+    ld = -(-K // 16) * 16 + x_extra
+    x = gpu(np.asarray(x_np, np.float32))
+    xq = torch.full((M, ld), 127, dtype=torch.uint8, device="cuda")   # NaN behind the columns
+    xs = torch.empty(M, -(-K // 128), device="cuda")
+    B.check(B.pw_scaled_quantize(x.data_ptr(), B.PW_TYPE_F32, M, K, K, 1, xq.data_ptr(), ld, xs.data_ptr()))
+    w, ldw = padded_codes(q)
+    if w_extra:
+        w2 = torch.full((E, N, ldw + w_extra), 127, dtype=torch.uint8, device="cuda")
+        w2[..., :ldw] = w
+        w, ldw = w2, ldw + w_extra
+    ws = gpu(s)
+    y = Strided(M, N, y_name, extra, base)
+    n = B.pw_scaled_gemm_workspace_bytes(M, N, K, E)
+    tmp = torch.full((n + 4096,), poison, dtype=torch.uint8, device="cuda")
+    o = gpu(np.asarray(off, np.int32)) if off is not None else None
+    B.check(B.pw_scaled_gemm(xq.data_ptr(), xs.data_ptr(), M, K, ld, w.data_ptr(), ws.data_ptr(), E, N,
+                             ldw, o.data_ptr() if o is not None else 0, y.ptr, TYPES[y_name], y.ld,
+                             tmp.data_ptr(), n))
+    st = B.pw_get_status()
+    assert st == B.PW_OK, B.pw_status_string(st)
+    assert bool((tmp[n:] == poison).all())
+    return y, S.values(*S.quantize(x.double().cpu().numpy(), 1), 1)
+
+
+def check(y, y_name, xv, v, off, K):
+    ref = S.gemm(xv, v, off)
+    mag = S.gemm(np.abs(xv), np.abs(v), off)
+    n = off[-1]
+    tol = sum_bound(-(-K // 128)) * mag[:n]
+    tol = tol + half_step(y_name) * (np.abs(ref[:n]) + tol) + (2.0 ** -25 if y_name == "f16" else 0)
+    got = y.np()
+    assert (np.abs(got[:n] - ref[:n]) <= tol).all(), float(np.max(np.abs(got[:n] - ref[:n]) / tol))
+    assert (got[n:] == -77.0).all() and y.outside_untouched()
+
+
+DENSE = [(1, 1, 1), (1, 128, 128), (4, 256, 128), (3, 300, 200), (17, 129, 136), (64, 512, 4096),
+         (65, 255, 1111), (128, 256, 256), (129, 257, 640), (300, 700, 384), (1, 40000, 256),
+         (2, 1000, 8192), (700, 9000, 128)]
+
+
+@pytest.mark.parametrize("y_name", list(TYPES))
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_product_dense(libpw, M, N, K, y_name):
+    rng = np.random.default_rng([M, N, K])
+    q, s, v = weights(1, N, K, 1)
+    y, xv = product(rng.normal(size=(M, K)), q, s, None, N, y_name)
+    check(y, y_name, xv, v, [0, M], K)
+
+
+GROUPED = [([0, 3], 256, 128), ([0, 0, 5, 5, 6], 300, 264), ([0, 1, 2, 3, 4, 5, 6, 7, 8], 384, 512),
+           ([0, 130, 130, 131, 400], 520, 384), ([0, 0, 0], 256, 128), ([0, 200, 260], 8192, 256)]
+
+
+@pytest.mark.parametrize("off,N,K", GROUPED)
+def test_product_grouped(libpw, off, N, K):
+    E, M = len(off) - 1, off[-1] + 9                       # nine rows behind the last group
+    rng = np.random.default_rng([E, N, K])
+    q, s, v = weights(E, N, K, 2)
+    y, xv = product(rng.normal(size=(M, K)), q, s, off, N, "bf16")
+    check(y, "bf16", xv, v, off, K)
+
+
+def test_product_many_experts(libpw):
+    E, N, K = 1024, 130, 128
+    rng = np.random.default_rng(7)
+    rows = rng.integers(0, 3, E)
+    off = np.concatenate([[0], np.cumsum(rows)])
+    q, s, v = weights(E, N, K, 3)
+    y, xv = product(rng.normal(size=(off[-1] + 1, K)), q, s, off, N, "f32")
+    check(y, "f32", xv, v, off, K)
+
+
+@pytest.mark.parametrize("extra,base,x_extra,w_extra", [(5, 0, 0, 0), (8, 0, 32, 16), (0, 1, 16, 0), (8, 8, 0, 48)])
+@pytest.mark.parametrize("y_name", list(TYPES))
+def test_product_strides(libpw, y_name, extra, base, x_extra, w_extra):
+    rng = np.random.default_rng(8)
+    q, s, v = weights(2, 392, 200, 4)
+    off = [0, 70, 133]
+    y, xv = product(rng.normal(size=(140, 200)), q, s, off, 392, y_name, extra, base, x_extra, w_extra)
+    check(y, y_name, xv, v, off, 200)
+
+
+def test_product_repeats_bit_for_bit(libpw):
+    """Units cut along K are joined in piece order, whichever CTA joins."""
+    rng = np.random.default_rng(9)
+    q, s, v = weights(1, 1536, 8192, 5)
+    x = rng.normal(size=(5, 8192))
+    first = product(x, q, s, None, 1536, "f32")[0].np()
+    for poison in (0, 0x7F, 0xFF):
+        assert np.array_equal(product(x, q, s, None, 1536, "f32", poison=poison)[0].np(), first)
+
+
+def test_product_non_finite_rows_stay_apart(libpw):
+    rng = np.random.default_rng(10)
+    q, s, v = weights(1, 256, 256, 6)
+    x = rng.normal(size=(6, 256)).astype(np.float32)
+    x[2, 3], x[4, 200] = np.nan, np.inf
+    y, xv = product(x, q, s, None, 256, "f32")
+    got = y.np()
+    assert np.isnan(got[[2, 4]]).all() and np.isfinite(got[[0, 1, 3, 5]]).all()
+    ref = S.gemm(xv[[0, 1, 3, 5]], v, [0, 4])
+    assert (np.abs(got[[0, 1, 3, 5]] - ref) <= (sum_bound(2) + U) * S.gemm(np.abs(xv[[0, 1, 3, 5]]), np.abs(v), [0, 4])).all()
+
+
+@pytest.mark.parametrize("off", [[0, 5, 3, 8], [0, 4, 20, 8], [-3, 2, 4, 8], [8, 0, 0, 0]])
+def test_bad_offsets_are_recorded(libpw, off):
+    """Rows outside [0, M] and groups that go backwards give no rows: nothing outside y is touched."""
+    import torch
+    M, N, K, E = 8, 256, 128, 3
+    q, s, _ = weights(E, N, K, 7)
+    w, ldw = padded_codes(q)
+    xq = torch.zeros(M, 128, dtype=torch.uint8, device="cuda")
+    xs, ws = torch.ones(M, 1, device="cuda"), gpu(s)
+    y = Strided(M, N, "f32", 0, 64)
+    n = B.pw_scaled_gemm_workspace_bytes(M, N, K, E)
+    tmp = torch.empty(n, dtype=torch.uint8, device="cuda")
+    o = gpu(np.asarray(off, np.int32))
+    B.check(B.pw_scaled_gemm(xq.data_ptr(), xs.data_ptr(), M, K, 128, w.data_ptr(), ws.data_ptr(), E, N, ldw,
+                             o.data_ptr(), y.ptr, B.PW_TYPE_F32, y.ld, tmp.data_ptr(), n))
+    assert B.pw_get_status() == B.PW_ERR_BOUNDS
+    assert y.outside_untouched()
+    got = y.np()
+    assert ((got == 0) | (got == -77.0)).all()
+
+
+def _layer(H, I, E, seed):
+    q1, s1, v1 = weights(E, 2 * I, H, seed)
+    q2, s2, v2 = weights(E, H, I, seed + 1)
+    s1, s2 = s1 * 4, s2 * 4
+    return (gpu(q1), gpu(s1), gpu(q2), gpu(s2)), v1 * 4, v2 * 4
+
+
+LAYERS = [(1, 2, 8, 256, 512, "f32", "f32"), (4, 2, 8, 256, 512, "bf16", "f32"), (33, 4, 12, 128, 384, "bf16", "bf16"),
+          (1, 1, 1, 128, 128, "f16", "f16"), (70, 3, 5, 384, 128, "f32", "bf16"), (300, 2, 3, 256, 256, "bf16", "f32")]
+
+
+@pytest.mark.parametrize("T,k,E,H,I,xt,yt", LAYERS)
+def test_layer(libpw, T, k, E, H, I, xt, yt):
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    rng = np.random.default_rng([T, k, E, H, I])
+    tensors, v1, v2 = _layer(H, I, E, 11)
+    ex = ScaledExperts(*tensors, max_tokens=T, k=k)
+    ex.workspace.fill_(0xFF)
+    idx = routing(T, E, k, 12, 0.1 if T > 4 else 0.0)
+    if T > 10:
+        idx[T - 3:] = -1
+    gate = rng.random((T, k)).astype(np.float32)
+    x = gpu(rng.normal(size=(T, H))).to(_torch_type(xt))
+    y = torch.full((T, H), -7.0, dtype=_torch_type(yt), device="cuda")
+    ex.forward(x, gpu(idx), gpu(gate), y)
+    assert B.pw_get_status() == B.PW_OK
+    ref, tol = moe_bound(x.double().cpu().numpy(), idx, gate, v1, v2)
+    tol = tol + half_step(yt) * (np.abs(ref) + tol) + 2.0 ** -25
+    got = y.double().cpu().numpy()
+    assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) / tol))
+    if T > 10:
+        assert (got[T - 3:] == 0).all()
+    # the bound itself is tight enough to see a wrong expert, gate or block
+    assert float(np.median(tol)) < 0.05 * float(np.sqrt((ref ** 2).mean()))
+
+
+def test_layer_bad_expert_is_recorded(libpw):
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    tensors, _, _ = _layer(128, 128, 4, 13)
+    ex = ScaledExperts(*tensors, max_tokens=4, k=2)
+    x = torch.randn(4, 128, device="cuda")
+    gate = torch.rand(4, 2, device="cuda")
+    good = gpu(np.array([[0, 1], [2, 3], [1, -1], [3, 0]], np.int32))
+    bad = good.clone()
+    bad[2, 1] = 4
+    a = ex.forward(x, good, gate)
+    assert B.pw_get_status() == B.PW_OK
+    b = ex.forward(x, bad, gate)
+    assert B.pw_get_status() == B.PW_ERR_BAD_EXPERT
+    assert bool((a == b).all())
+
+
+def test_layer_after_the_router_in_a_graph(libpw):
+    """Router, remap, expert layer: captured once on another stream, replayed on new activations;
+    equal to the calls made one by one."""
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    cfg = CONFIGS["qwen2_57b_a14b"].scaled(H=256, I=128, E=16)
+    T, E, H, k = 24, cfg.E, cfg.H, cfg.k
+    tensors, _, _ = _layer(H, cfg.I, E, 14)
+    ex = ScaledExperts(*tensors, max_tokens=T, k=k)
+    rc = B.pw_route_cfg(k=k, renorm=1, policy=0, threshold=0.15, critical_n=10)
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    wr = torch.randn(E, H, device="cuda") * 0.1
+    logits = torch.empty(T, E, device="cuda")
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    gate = torch.empty(T, k, device="cuda")
+    y = torch.empty(T, H, device="cuda").bfloat16()
+
+    def step(st):
+        B.check(B.pw_route_topk(x.data_ptr(), wr.data_ptr(), 0, T, H, E, rc, logits.data_ptr(),
+                                idx.data_ptr(), gate.data_ptr(), st))
+        B.check(B.pw_remap(logits.data_ptr(), idx.data_ptr(), gate.data_ptr(), T, E, rc, 0, 0, st))
+        ex.forward(x, idx, gate, y, stream=st)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step(s.cuda_stream)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        x.normal_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        step(torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert bool((y == got).all()) and bool(got.isfinite().all())
+    assert B.pw_get_status() == B.PW_OK
+
+
+def test_layer_two_streams_with_their_own_workspaces(libpw):
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    H, I, E, T, k = 512, 512, 8, 40, 2
+    tensors, _, _ = _layer(H, I, E, 15)
+    xs = [torch.randn(T, H, device="cuda").bfloat16() for _ in range(2)]
+    idx, gate = gpu(routing(T, E, k, 16)), torch.rand(T, k, device="cuda")
+    ex = [ScaledExperts(*tensors, max_tokens=T, k=k) for _ in range(2)]
+    want = [ex[0].forward(x, idx, gate).clone() for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ys = [torch.empty_like(x) for x in xs]
+    for _ in range(20):
+        for i in range(2):
+            ex[i].forward(xs[i], idx, gate, ys[i], stream=streams[i].cuda_stream)
+    torch.cuda.synchronize()
+    assert all(bool((a == b).all()) for a, b in zip(ys, want))
+    assert B.pw_get_status() == B.PW_OK
+
+
+def test_quantized_weights_object(libpw):
+    """quantize_weights: 128 x 128 blocks of each matrix, odd sizes included, and a layer on them
+    close to the unquantised one (both roundings are at most 2^-4 of a value)."""
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts, quantize_weights
+    w = torch.randn(3, 200, 150, device="cuda")
+    q, s = quantize_weights(w)
+    for e in range(3):
+        wq, wsc = S.quantize(w[e].double().cpu().numpy(), 128)
+        assert np.array_equal(q[e, :, :150].cpu().numpy(), wq)
+        assert np.array_equal(s[e].double().cpu().numpy(), wsc)
+    E, H, I, T, k = 4, 256, 128, 9, 2
+    w1, w2 = torch.randn(E, 2 * I, H, device="cuda") * 0.05, torch.randn(E, H, I, device="cuda") * 0.05
+    ex = ScaledExperts(*quantize_weights(w1.bfloat16()), *quantize_weights(w2.bfloat16()), max_tokens=T, k=k)
+    idx, gate = routing(T, E, k, 17), np.random.default_rng(18).random((T, k)).astype(np.float32)
+    x = torch.randn(T, H, device="cuda")
+    y = ex.forward(x, gpu(idx), gpu(gate)).double().cpu().numpy()
+    v = [[S.values(*S.quantize(m[e].bfloat16().double().cpu().numpy(), 128), 128) for e in range(E)] for m in (w1, w2)]
+    ref, tol = moe_bound(x.double().cpu().numpy(), idx, gate, np.stack(v[0]), np.stack(v[1]))
+    assert (np.abs(y - ref) <= tol + U * np.abs(ref)).all()
+    assert B.pw_get_status() == B.PW_OK

@@ -21,6 +21,7 @@
 #include "pw_route.cuh"
 #include "pw_rows.cuh"
 #include "pw_scaled.cuh"
+#include "pw_scaled_few.cuh"
 #include "pw_table.cuh"
 #include "pw_tc.cuh"
 

@@ -40,10 +40,13 @@ ScaledDevice g_scaled_dev[kMaxDevices];
 std::mutex g_scaled_mu;
 
 template <typename F>
+bool shared_ready(F* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+template <typename F>
 bool scaled_kernel_ready(F* kernel) {
   cudaFuncAttributes a;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           pw::k7::smem_bytes(PW_MAX_EXPERTS)) != cudaSuccess ||
+  if (!shared_ready(kernel, pw::k7::smem_bytes(PW_MAX_EXPERTS)) ||
       cudaFuncGetAttributes(&a, kernel) != cudaSuccess)
     return false;
   // the register split of the warpgroups has to fit what the block is launched with
@@ -57,10 +60,13 @@ pw_status scaled_device(DeviceInfo** di) {
   if (cudaGetDevice(&dev) != cudaSuccess) return PW_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_scaled_mu);
   if (g_scaled_dev[dev].ready) return PW_OK;
-  if (cudaFuncSetAttribute(pw::sort_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           2 * pw::kSortWarps * PW_MAX_EXPERTS) != cudaSuccess ||
-      cudaFuncSetAttribute(pw::sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (4 + 2 * pw::kSortWarps) * PW_MAX_EXPERTS) != cudaSuccess)
+  const int few = pw::k8::smem_bytes(PW_MAX_EXPERTS);
+  if (!shared_ready(pw::sort_count_kernel, 2 * pw::kSortWarps * PW_MAX_EXPERTS) ||
+      !shared_ready(pw::sort_place_kernel, (4 + 2 * pw::kSortWarps) * PW_MAX_EXPERTS) ||
+      !shared_ready(pw::k8::few_kernel<true, PW_TYPE_F32>, few) ||
+      !shared_ready(pw::k8::few_kernel<false, PW_TYPE_F32>, few) ||
+      !shared_ready(pw::k8::few_kernel<false, PW_TYPE_BF16>, few) ||
+      !shared_ready(pw::k8::few_kernel<false, PW_TYPE_F16>, few))
     return PW_ERR_CUDA;
   if (!scaled_kernel_ready(pw::k7::scaled_kernel<true, PW_TYPE_F32>) ||
       !scaled_kernel_ready(pw::k7::scaled_kernel<false, PW_TYPE_F32>) ||
@@ -126,6 +132,10 @@ struct ScaledCall {
   int32_t* counter;
 };
 
+// Rows per expert (on average over the experts that can have one) up to which the few-rows kernel
+// is used.
+constexpr int kFewRows = 48;
+
 int part_rows(int M) { return static_cast<int>(align_up(std::min(M, pw::k7::kTileM), 32)); }
 size_t part_bytes(int M) {
   return sizeof(float) * 2 * kScaledMaxGrid * pw::k7::kTileN * static_cast<size_t>(part_rows(M));
@@ -134,9 +144,10 @@ size_t part_bytes(int M) {
 pw_status launch_scaled(const ScaledCall& c, int sms, cudaStream_t st) {
   pw::k7::Params p;
   const bool gated = c.hq != nullptr;
+  const bool few = c.M <= kFewRows * std::min(c.E, c.M);
   if (!byte_map(&p.xmap, c.xq, c.K, c.M, 1, c.ldx, 2, pw::k7::kTileM) ||
       !byte_map(&p.xsmall, c.xq, c.K, c.M, 1, c.ldx, 2, pw::k7::kSmallRows) ||
-      !byte_map(&p.wmap, c.wq, c.K, c.N, c.E, c.ldw, 3, gated ? 64 : pw::k7::kTileN))
+      !byte_map(&p.wmap, c.wq, c.K, c.N, c.E, c.ldw, 3, gated ? (few ? 128 : 64) : pw::k7::kTileN))
     return PW_ERR_CUDA;
   p.sx = c.xs;
   p.sw = c.ws;
@@ -158,6 +169,15 @@ pw_status launch_scaled(const ScaledCall& c, int sms, cudaStream_t st) {
   p.rcap = part_rows(c.M);
   p.counter = c.counter;
   const dim3 grid(std::min(sms, kScaledMaxGrid)), block(pw::k7::kThreads);
+  if (few) {
+    const size_t smem = pw::k8::smem_bytes(c.E);
+    if (gated) return launch_dependent(pw::k8::few_kernel<true, PW_TYPE_F32>, grid, block, smem, st, p);
+    if (c.y_type == PW_TYPE_F32)
+      return launch_dependent(pw::k8::few_kernel<false, PW_TYPE_F32>, grid, block, smem, st, p);
+    if (c.y_type == PW_TYPE_BF16)
+      return launch_dependent(pw::k8::few_kernel<false, PW_TYPE_BF16>, grid, block, smem, st, p);
+    return launch_dependent(pw::k8::few_kernel<false, PW_TYPE_F16>, grid, block, smem, st, p);
+  }
   const size_t smem = pw::k7::smem_bytes(c.E);
   if (gated) return launch_dependent(pw::k7::scaled_kernel<true, PW_TYPE_F32>, grid, block, smem, st, p);
   if (c.y_type == PW_TYPE_F32)

@@ -50,7 +50,8 @@ constexpr int kOffBar = kStages * kStageBytes;
 constexpr int kNumBars = 2 * kStages + 4 + 1;
 constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) / 16) * 16;
 constexpr int kOffAmax = kOffMisc + 32;
-constexpr int kOffTiles = kOffAmax + 2 * kTileM * 4;  // [E + 1] row tiles before each expert
+constexpr int kOffStage = kOffAmax + 2 * kTileM * 4;  // output staging, 32 rows x 80 bytes a warp
+constexpr int kOffTiles = kOffStage + (kEpiThreads / 32) * 32 * 80;  // [E + 1] row tiles before each expert
 constexpr int smem_bytes(int E) { return kOffTiles + 2 * (E + 1) * 4; }
 static_assert(smem_bytes(PW_MAX_EXPERTS) <= 227 * 1024, "shared memory budget");
 
@@ -78,13 +79,20 @@ struct alignas(64) Params {
 struct Sched {
   int units, waves, rem, pieces, run;  // run: K blocks of the remainder, cut into `pieces`
 };
+// EVEN: the remainder is cut into equal runs over all CTAs, wherever units end (joins are cheap: few
+// rows).  Otherwise every unit of it is cut into the same number of pieces, so that a unit has the
+// fewest pieces to join and none is cut for less than its share of a whole CTA.
+template <bool EVEN>
 __device__ __forceinline__ Sched make_sched(int units, int kb, int grid) {
   Sched s;
   s.units = units;
   s.waves = units / grid;
   s.rem = units - s.waves * grid;
   s.run = s.rem * kb;
-  s.pieces = min(grid, max(s.rem, s.run / kMinPiece));
+  if (EVEN)
+    s.pieces = min(grid, max(s.rem, s.run / kMinPiece));
+  else
+    s.pieces = s.rem ? s.rem * max(1, min(grid / s.rem, kb / kMinPiece)) : 0;
   return s;
 }
 __device__ __forceinline__ int piece_begin(const Sched& s, int p) {
@@ -129,9 +137,24 @@ __device__ __forceinline__ bool get_piece(const Sched& s, int kb, int i, Piece& 
   return true;
 }
 
+// The 256 epilogue threads (threads 128-383), after their partials are written: true in all of them
+// if this is the last of the unit's `count` pieces; the others' partials are then visible.
+constexpr int kEpiBarrier = 1;
+__device__ __forceinline__ bool last_piece(int32_t* counter, int count, int* s_last) {
+  named_sync(kEpiBarrier, kEpiThreads);
+  if (threadIdx.x == 128) {
+    __threadfence();  // releases what the barrier gathered
+    *s_last = atomicAdd(counter, 1) == count - 1;
+    __threadfence();
+  }
+  named_sync(kEpiBarrier, kEpiThreads);
+  return *s_last != 0;
+}
+
 struct Unit {
-  int e, row0, rows, n;  // expert, first row, rows (<= 128), column tile
+  int e, row0, rows, n;  // expert, first row, rows (<= the tile's), column tile
 };
+template <int TM>
 __device__ __forceinline__ Unit find_unit(const Params& p, const int* tiles, const int* first, int u) {
   const int v = u / p.nt;
   int lo = 0, hi = p.E - 1;  // the last expert with tiles[e] <= v that has tiles
@@ -146,9 +169,40 @@ __device__ __forceinline__ Unit find_unit(const Params& p, const int* tiles, con
   const int local = u - p.nt * tiles[lo];
   r.n = local / mt;
   const int m = local - r.n * mt;
-  r.row0 = first[lo] + m * kTileM;
-  r.rows = min(kTileM, first[lo + 1] - r.row0);
+  r.row0 = first[lo] + m * TM;
+  r.rows = min(TM, first[lo + 1] - r.row0);
   return r;
+}
+
+// ---- waits ----
+// Bounded wait on an mbarrier, as mbar_wait, but the clock and the limit (a global load) are read
+// only after several suspended tries: this kernel hands tensor-memory stages back and forth every
+// few hundred cycles, and a wait that reads the limit first costs more than a stage takes (M 4736,
+// N 1024, K 16384: 98.9 us with mbar_wait, 88.8 us so).
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const unsigned long long t0 = global_ns();
+  const unsigned long long limit = wait_limit_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > limit) {
+      set_status(PW_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, abort_flag);
+}
+
+// The whole warp waits; the answer is the same in every lane, so no later warp-wide step meets a
+// split warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
 }
 
 // ---- tcgen05 / TMA ----
@@ -161,13 +215,25 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 // kind::f8f6f4, e4m3 x e4m3 (both K-major) -> fp32, M = 128, N = 256.
 constexpr uint32_t kInstr = (1u << 4) | ((kTileN >> 3) << 17) | ((kTileM >> 4) << 24);
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+                                       uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(kInstr), "r"(accumulate)
+      ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"(accumulate)
       : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -215,34 +281,97 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// acc[0..31] += r * s, two elements an instruction.
 __device__ __forceinline__ void fold32(float* acc, const uint32_t (&r)[32], float s) {
+  const uint64_t s2 = (static_cast<uint64_t>(__float_as_uint(s)) << 32) | __float_as_uint(s);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
+  for (int i = 0; i < 32; i += 2) {
+    const uint64_t x = (static_cast<uint64_t>(r[i + 1]) << 32) | r[i];
+    uint64_t a = (static_cast<uint64_t>(__float_as_uint(acc[i + 1])) << 32) | __float_as_uint(acc[i]);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(x), "l"(s2));
+    acc[i] = __uint_as_float(static_cast<uint32_t>(a));
+    acc[i + 1] = __uint_as_float(static_cast<uint32_t>(a >> 32));
+  }
 }
 
 // SiLU(g) * u.  The hardware exponential and reciprocal (errors of a few 2^-22) are far below the
 // 2^-4 step of the e4m3 value that h becomes.
 __device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// 128 columns of one row (a thread): stores of 16 bytes where alignment and the edge allow.
+// A warp's 32 rows x 128 columns (a thread holds one row's) to y, through a staging buffer of 32 rows
+// x 64 bytes (rows 80 bytes apart: conflict free both ways), so that a store instruction writes
+// 64-byte runs of 8 rows and not 16 bytes of 32.  rows: rows of the warp that exist; n: first column.
+constexpr int kStageRow = 80;
 template <int TY>
-__device__ __forceinline__ void store_row(void* y, size_t at, int n, int N, int vec, const float (&acc)[128]) {
-  constexpr int S = ElemSize<TY>::value;
-  if (vec && n + 128 <= N) {
+__device__ __forceinline__ void store_rows(uint8_t* stage, void* y, size_t row0, size_t ld, int rows, int n,
+                                           int N, int vec, const float (&acc)[128], int lane) {
+  constexpr int S = ElemSize<TY>::value, C = 64 / S;  // columns of a run
 #pragma unroll
-    for (int c = 0; c < 128; c += 8) {
-      float v[8];
+  for (int c0 = 0; c0 < 128; c0 += C) {
+    if (n + c0 >= N) break;
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
-      store_elems<TY, 8>(elem_at(y, at + n + c, S), v);
+    for (int c = 0; c < C; c += 16 / S) {
+      float v[16 / S];
+#pragma unroll
+      for (int i = 0; i < 16 / S; ++i) v[i] = acc[c0 + c + i];
+      store_elems<TY, 16 / S>(stage + lane * kStageRow + c * S, v);
     }
-  } else {
+    __syncwarp();
+    if (vec && n + c0 + C <= N) {
 #pragma unroll
-    for (int c = 0; c < 128; ++c)
-      if (n + c < N) {
-        const float v[1] = {acc[c]};
-        store_elems<TY, 1>(elem_at(y, at + n + c, S), v);
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), c = (lane & 3) * 16;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kStageRow + c);
+        if (r < rows)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(y) + ((row0 + r) * ld + n + c0) * S + c) = w;
       }
+    } else {
+      for (int i = 0; i < 32 * C / 32; ++i) {
+        const int r = (32 / C) * i + lane / C, c = lane % C;
+        if (r < rows && n + c0 + c < N) {
+          void* d = elem_at(y, (row0 + r) * ld + n + c0 + c, S);
+          if (S == 4)
+            *static_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(stage + r * kStageRow + c * 4);
+          else
+            *static_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(stage + r * kStageRow + c * 2);
+        }
+      }
+    }
+  }
+}
+
+// Row tiles (of TM rows) before each expert, from the offsets: tiles[E + 1], first[E + 1] in shared
+// memory; offsets that decrease or leave [0, M] give no rows and are recorded.  Whole block.
+template <int TM>
+__device__ __forceinline__ void row_tiles(const Params& p, int* tiles, int* first) {
+  const int E = p.E;
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+    const int o = p.offsets ? p.offsets[e] : (e ? p.M : 0);
+    first[e] = min(max(o, 0), p.M);
+    if (o < 0 || o > p.M) set_status(PW_ERR_BOUNDS);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      int v = 0;
+      if (e < E) {
+        const int rows = first[e + 1] - first[e];
+        if (rows < 0) set_status(PW_ERR_BOUNDS);
+        v = rows > 0 ? (rows + TM - 1) / TM : 0;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+      }
+      if (e < E) tiles[e + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) tiles[0] = 0;
   }
 }
 
@@ -261,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
   float* s_amax = reinterpret_cast<float*>(smem + kOffAmax);
   int* s_tiles = reinterpret_cast<int*>(smem + kOffTiles);  // [E + 1]
   const int E = p.E;
-  int* s_first = s_tiles + E + 1;                           // [E + 1] offsets
+  int* s_first = s_tiles + E + 1;                           // [E + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (smem_u32(smem) & 1023) {  // the swizzled buffers start on 1024-byte boundaries
@@ -293,76 +422,55 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
   }
   griddep_wait();
   griddep_launch();
-  // row tiles before each expert; offsets that decrease or leave [0, M] give no rows
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
-    const int o = p.offsets ? p.offsets[e] : (e ? p.M : 0);
-    s_first[e] = min(max(o, 0), p.M);
-    if (o < 0 || o > p.M) set_status(PW_ERR_BOUNDS);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      int v = 0;
-      if (e < E) {
-        const int rows = s_first[e + 1] - s_first[e];
-        if (rows < 0 && blockIdx.x == 0) set_status(PW_ERR_BOUNDS);
-        v = rows > 0 ? (rows + kTileM - 1) / kTileM : 0;
-      }
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
-      }
-      if (e < E) s_tiles[e + 1] = carry + v;
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) s_tiles[0] = 0;
-  }
+  row_tiles<kTileM>(p, s_tiles, s_first);
   k5::tc_fence_before();
   __syncthreads();
   k5::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const Sched sched = make_sched(s_tiles[E] * p.nt, p.kb, gridDim.x);
+  const Sched sched = make_sched<false>(s_tiles[E] * p.nt, p.kb, gridDim.x);
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    if (warp == 0 && lane == 0) {
+    const bool leader = elect_one();  // one lane issues; control flow and operands stay uniform
+    if (warp == 0) {
       // ---------------- producer ----------------
       uint32_t g = 0;
       Piece pc;
       bool ok = true;
       for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
-        const Unit u = find_unit(p, s_tiles, s_first, pc.unit);
+        const Unit u = find_unit<kTileM>(p, s_tiles, s_first, pc.unit);
         const bool whole = u.rows > kTileM / 2;
         const int boxes = (u.rows + kSmallRows - 1) / kSmallRows;
         const uint32_t bytes = kBBytes + (whole ? kABytes : boxes * kSmallRows * kBlk);
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
           const int s = g % kStages;
-          if (!(ok = k5::wait_bar(&empty[s], ((g / kStages) & 1) ^ 1, abort_flag))) break;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          const uint32_t a = smem_base + s * kStageBytes, w = a + kABytes;
-          if (GATED) {  // 64 gate, 64 up, 64 gate, 64 up rows: each epilogue half has both
-            for (int q = 0; q < 4; ++q)
-              tma_3d(w + q * (kBBytes / 4), &p.wmap, b * kBlk,
-                     (q & 1 ? p.I : 0) + u.n * 128 + (q >> 1) * 64, u.e, &full[s]);
-          } else {
-            tma_3d(w, &p.wmap, b * kBlk, u.n * kTileN, u.e, &full[s]);
+          if (!(ok = warp_wait(&empty[s], ((g / kStages) & 1) ^ 1, abort_flag))) break;
+          if (leader) {
+            mbar_arrive_expect_tx(&full[s], bytes);
+            const uint32_t a = smem_base + s * kStageBytes, w = a + kABytes;
+            if (GATED) {  // 64 gate, 64 up, 64 gate, 64 up rows: each epilogue half has both
+              for (int q = 0; q < 4; ++q)
+                tma_3d(w + q * (kBBytes / 4), &p.wmap, b * kBlk,
+                       (q & 1 ? p.I : 0) + u.n * 128 + (q >> 1) * 64, u.e, &full[s]);
+            } else {
+              tma_3d(w, &p.wmap, b * kBlk, u.n * kTileN, u.e, &full[s]);
+            }
+            if (whole) {
+              tma_2d(a, &p.xmap, b * kBlk, u.row0, &full[s]);
+            } else {
+              for (int q = 0; q < boxes; ++q)
+                tma_2d(a + q * kSmallRows * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kSmallRows, &full[s]);
+            }
           }
-          if (whole) {
-            tma_2d(a, &p.xmap, b * kBlk, u.row0, &full[s]);
-          } else {
-            for (int q = 0; q < boxes; ++q)
-              tma_2d(a + q * kSmallRows * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kSmallRows, &full[s]);
-          }
+          __syncwarp();
         }
       }
       // every issued copy has landed before the block exits
-      for (uint32_t x = (g > kStages ? g - kStages : 0); x < g; ++x)
-        mbar_wait(&full[x % kStages], (x / kStages) & 1);
-    } else if (warp == 1 && lane == 0) {
+      if (leader)
+        for (uint32_t x = (g > kStages ? g - kStages : 0); x < g; ++x)
+          mbar_wait(&full[x % kStages], (x / kStages) & 1);
+    } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
       uint32_t g = 0;
       Piece pc;
@@ -370,20 +478,25 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
       for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
           const int s = g % kStages, t = g & 1;
-          if (!(ok = k5::wait_bar(&acc_empty[t], ((g >> 1) & 1) ^ 1, abort_flag))) break;
-          if (!(ok = k5::wait_bar(&full[s], (g / kStages) & 1, abort_flag))) break;
-          k5::tc_fence_after();
+          if (!(ok = warp_wait(&full[s], (g / kStages) & 1, abort_flag))) break;
           const uint64_t ad = sw128_desc(smem_base + s * kStageBytes);
           const uint64_t bd = sw128_desc(smem_base + s * kStageBytes + kABytes);
-          const uint32_t d = tmem_base + t * kAccCols;
+          if (!(ok = warp_wait(&acc_empty[t], ((g >> 1) & 1) ^ 1, abort_flag))) break;
+          k5::tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f8(d, ad + 2 * j, bd + 2 * j, j > 0);  // 32 bytes of K each
-          k5::mma_commit(&empty[s]);
-          k5::mma_commit(&acc_full[t]);
+            for (int j = 0; j < 4; ++j)  // 32 bytes of K each
+              mma_f8(tmem_base + t * kAccCols, ad + 2 * j, bd + 2 * j, kInstr, j > 0);
+            k5::mma_commit(&empty[s]);
+            k5::mma_commit(&acc_full[t]);
+          }
+          __syncwarp();
         }
       }
-      k5::mma_commit(mma_done);
-      mbar_wait(mma_done, 0);
+      if (leader) {
+        k5::mma_commit(mma_done);
+        mbar_wait(mma_done, 0);
+      }
     }
   } else {
     // ---------------- epilogue ----------------
@@ -395,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
     Piece pc;
     bool dead = false;  // a wait gave up: keep every barrier, write zeros
     for (int i = 0; get_piece(sched, p.kb, i, pc); ++i) {
-      const Unit u = find_unit(p, s_tiles, s_first, pc.unit);
+      const Unit u = find_unit<kTileM>(p, s_tiles, s_first, pc.unit);
       const bool mine = quarter * 32 < u.rows;  // the warp has rows
       const bool live = r < u.rows;
       const size_t row = static_cast<size_t>(u.row0) + (live ? r : u.rows - 1);
@@ -418,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           w0_next = __ldg(sw0 + b + 1);
           if (GATED) w1_next = __ldg(sw1 + b + 1);
         }
-        if (!__all_sync(0xffffffffu, k5::wait_bar(&acc_full[t], (g >> 1) & 1, abort_flag))) {
+        if (!warp_wait(&acc_full[t], (g >> 1) & 1, abort_flag)) {
           dead = true;
         } else {
           k5::tc_fence_after();
@@ -459,29 +572,23 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
 #pragma unroll
           for (int c = 0; c < 128; ++c) __stcg(d + static_cast<size_t>(c) * p.rcap, acc[c]);
         }
-        __threadfence();
-        named_sync(1, kEpiThreads);
-        if (threadIdx.x == 128)
-          *s_last = atomicAdd(p.counter + (pc.unit - sched.waves * static_cast<int>(gridDim.x)), 1) ==
-                    pc.count - 1;
-        named_sync(1, kEpiThreads);
-        if (!*s_last) continue;
-        __threadfence();
+        if (!last_piece(p.counter + (pc.unit - sched.waves * static_cast<int>(gridDim.x)), pc.count, s_last))
+          continue;
         if (live) {
           const int j = pc.unit - sched.waves * static_cast<int>(gridDim.x);
 #pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 16) {
-            float v[16];
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            float v[32];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = 0.0f;
+            for (int c = 0; c < 32; ++c) v[c] = 0.0f;
             for (int q = pc.first; q < pc.first + pc.count; ++q) {
               const int slot = 2 * q + (piece_begin(sched, q) / p.kb == j ? 0 : 1);
               const float* d = p.part + slot * slot_floats + static_cast<size_t>(half * 128 + c0) * p.rcap + r;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) v[c] += __ldcg(d + static_cast<size_t>(c) * p.rcap);
+              for (int c = 0; c < 32; ++c) v[c] += __ldcg(d + static_cast<size_t>(c) * p.rcap);
             }
 #pragma unroll
-            for (int c = 0; c < 16; ++c) acc[c0 + c] = v[c];
+            for (int c = 0; c < 32; ++c) acc[c0 + c] = v[c];
           }
         }
       }
@@ -492,9 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           acc[c] = gated(acc[c], acc[64 + c]);
           m = fmaxf(m, finite_abs(acc[c]));
         }
-        named_sync(1, kEpiThreads);  // the previous tile's maxima are read
+        named_sync(kEpiBarrier, kEpiThreads);  // the previous tile's maxima are read
         s_amax[half * kTileM + r] = m;
-        named_sync(1, kEpiThreads);
+        named_sync(kEpiBarrier, kEpiThreads);
         m = fmaxf(s_amax[r], s_amax[kTileM + r]);
         const int ex = scale_exponent(m);
         const float inv = pow2(-ex);
@@ -511,8 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
             d[c / 16] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-      } else if (live) {
-        store_row<TO>(p.y, row * p.ld_y, u.n * kTileN + half * 128, p.N, p.vec, acc);
+      } else if (mine) {
+        store_rows<TO>(smem + kOffStage + ew * 32 * kStageRow, p.y, static_cast<size_t>(u.row0) + quarter * 32,
+                       p.ld_y, min(32, u.rows - quarter * 32), u.n * kTileN + half * 128, p.N, p.vec, acc, lane);
       }
     }
   }

@@ -271,7 +271,7 @@ pw_status launch_combine_grad(const void* dy, const void* o, int T, int k, int H
 
 // Workspace of pw_moe_scaled_forward.
 struct ScaledWorkspace {
-  size_t pos, src, offsets, sort, counter, xq, xs, hq, hs, o, part, total;
+  size_t pos, src, offsets, sort, counter, xq, xs, hq, hs, o, part[2], total;
 };
 ScaledWorkspace scaled_ws(int T, int k, int E, int H, int I) {
   ScaledWorkspace w;
@@ -292,7 +292,9 @@ ScaledWorkspace scaled_ws(int T, int k, int E, int H, int I) {
   w.hq = take(n * I);
   w.hs = take(4 * n * (I / 128));
   w.o = take(4 * n * H);
-  w.part = take(part_bytes(static_cast<int>(n)));
+  // one set of partials for each product: the second starts while the first still joins
+  w.part[0] = take(part_bytes(static_cast<int>(n)));
+  w.part[1] = take(part_bytes(static_cast<int>(n)));
   w.total = at;
   return w;
 }
@@ -518,7 +520,7 @@ pw_status pw_moe_scaled_forward(const pw_scaled_experts* ex, const void* x, int 
   c.hs = hs;
   c.I = I;
   c.counter = counter;
-  c.part = reinterpret_cast<float*>(base + w.part);
+  c.part = reinterpret_cast<float*>(base + w.part[0]);
   s = launch_scaled(c, di->sms, st);
   if (s != PW_OK) return s;
   ScaledCall d = {};
@@ -537,7 +539,7 @@ pw_status pw_moe_scaled_forward(const pw_scaled_experts* ex, const void* x, int 
   d.y_type = PW_TYPE_F32;
   d.ld_y = H;
   d.counter = counter + kScaledMaxGrid;
-  d.part = c.part;
+  d.part = reinterpret_cast<float*>(base + w.part[1]);
   s = launch_scaled(d, di->sms, st);
   if (s != PW_OK) return s;
   return launch_combine(o, PW_TYPE_F32, T, k, H, H, pos, gate, y, y_type, H, st);

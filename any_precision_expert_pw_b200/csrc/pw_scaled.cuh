@@ -16,6 +16,12 @@
 // finishes last (partials and a counter in the workspace; the sum runs in piece order whoever joins,
 // so results repeat bit for bit).  Nobody waits for another CTA.
 //
+// Order of launches: a launch before the one in front of this one has completed when this one starts
+// (every kernel here lets its dependents start only after its own wait), so the offsets and the
+// weights are read at once, and only the rows, their scales, the counters and the outputs wait for
+// the launch in front.  The first weight tiles of a CTA then travel while slower CTAs of that launch
+// still finish.
+//
 // Warps: 0 TMA producer (4 stages of 16 KB rows + 32 KB weights; few rows: only their 16-row boxes),
 // 1 MMA issuer (4 MMAs of 128 x 256 x 32 a block into one of two tensor-memory stages), 2 tensor
 // memory, 4-11 epilogue (two warps per 32-row quarter, 128 columns each; warps whose rows are all
@@ -142,10 +148,10 @@ __device__ __forceinline__ bool get_piece(const Sched& s, int kb, int i, Piece& 
 constexpr int kEpiBarrier = 1;
 __device__ __forceinline__ bool last_piece(int32_t* counter, int count, int* s_last) {
   named_sync(kEpiBarrier, kEpiThreads);
-  if (threadIdx.x == 128) {
-    __threadfence();  // releases what the barrier gathered
-    *s_last = atomicAdd(counter, 1) == count - 1;
-    __threadfence();
+  if (threadIdx.x == 128) {  // releases what the barrier gathered, acquires what others released
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    *s_last = before == count - 1;
   }
   named_sync(kEpiBarrier, kEpiThreads);
   return *s_last != 0;
@@ -281,6 +287,15 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// The same for two buffers, one wait.
+__device__ __forceinline__ void tmem_wait2(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  tmem_wait(a);
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(b[i]), "+r"(b[i + 1]), "+r"(b[i + 2]), "+r"(b[i + 3]), "+r"(b[i + 4]),
+                 "+r"(b[i + 5]), "+r"(b[i + 6]), "+r"(b[i + 7]));
+}
+
 // acc[0..31] += r * s, two elements an instruction.
 __device__ __forceinline__ void fold32(float* acc, const uint32_t (&r)[32], float s) {
   const uint64_t s2 = (static_cast<uint64_t>(__float_as_uint(s)) << 32) | __float_as_uint(s);
@@ -347,7 +362,7 @@ template <int TM>
 __device__ __forceinline__ void row_tiles(const Params& p, int* tiles, int* first) {
   const int E = p.E;
   for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-    const int o = p.offsets ? p.offsets[e] : (e ? p.M : 0);
+    const int o = p.offsets ? __ldcg(p.offsets + e) : (e ? p.M : 0);
     first[e] = min(max(o, 0), p.M);
     if (o < 0 || o > p.M) set_status(PW_ERR_BOUNDS);
   }
@@ -420,8 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  griddep_wait();
-  griddep_launch();
   row_tiles<kTileM>(p, s_tiles, s_first);
   k5::tc_fence_before();
   __syncthreads();
@@ -435,20 +448,48 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
     const bool leader = elect_one();  // one lane issues; control flow and operands stay uniform
     if (warp == 0) {
       // ---------------- producer ----------------
+      // the first kStages weight tiles are on their way before the launch in front has ended; the
+      // rows (its output) follow
       uint32_t g = 0;
       Piece pc;
       bool ok = true;
+      auto rows_of = [&](const Unit& u, int b, uint32_t stage) {
+        const uint32_t a = smem_base + stage * kStageBytes;
+        if (u.rows > kTileM / 2) {
+          tma_2d(a, &p.xmap, b * kBlk, u.row0, &full[stage]);
+        } else {
+          for (int q = 0; q * kSmallRows < u.rows; ++q)
+            tma_2d(a + q * kSmallRows * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kSmallRows, &full[stage]);
+        }
+      };
+      auto follow = [&]() {  // the rows of the blocks before g
+        griddep_wait();
+        if (leader) {
+          uint32_t h = 0;
+          Piece q;
+          for (int i = 0; h < g && get_piece(sched, p.kb, i, q); ++i) {
+            const Unit u = find_unit<kTileM>(p, s_tiles, s_first, q.unit);
+            for (int b = q.k0; b < q.k1 && h < g; ++b, ++h) rows_of(u, b, h);
+          }
+          griddep_launch();
+        }
+        __syncwarp();
+      };
+      bool waited = false;
       for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
         const Unit u = find_unit<kTileM>(p, s_tiles, s_first, pc.unit);
-        const bool whole = u.rows > kTileM / 2;
         const int boxes = (u.rows + kSmallRows - 1) / kSmallRows;
-        const uint32_t bytes = kBBytes + (whole ? kABytes : boxes * kSmallRows * kBlk);
+        const uint32_t bytes = kBBytes + (u.rows > kTileM / 2 ? kABytes : boxes * kSmallRows * kBlk);
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
+          if (g == kStages && !waited) {
+            follow();
+            waited = true;
+          }
           const int s = g % kStages;
           if (!(ok = warp_wait(&empty[s], ((g / kStages) & 1) ^ 1, abort_flag))) break;
           if (leader) {
             mbar_arrive_expect_tx(&full[s], bytes);
-            const uint32_t a = smem_base + s * kStageBytes, w = a + kABytes;
+            const uint32_t w = smem_base + s * kStageBytes + kABytes;
             if (GATED) {  // 64 gate, 64 up, 64 gate, 64 up rows: each epilogue half has both
               for (int q = 0; q < 4; ++q)
                 tma_3d(w + q * (kBBytes / 4), &p.wmap, b * kBlk,
@@ -456,16 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
             } else {
               tma_3d(w, &p.wmap, b * kBlk, u.n * kTileN, u.e, &full[s]);
             }
-            if (whole) {
-              tma_2d(a, &p.xmap, b * kBlk, u.row0, &full[s]);
-            } else {
-              for (int q = 0; q < boxes; ++q)
-                tma_2d(a + q * kSmallRows * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kSmallRows, &full[s]);
-            }
+            if (waited) rows_of(u, b, s);
           }
           __syncwarp();
         }
       }
+      if (!waited) follow();
       // every issued copy has landed before the block exits
       if (leader)
         for (uint32_t x = (g > kStages ? g - kStages : 0); x < g; ++x)
@@ -507,22 +544,31 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
     uint32_t g = 0;
     Piece pc;
     bool dead = false;  // a wait gave up: keep every barrier, write zeros
-    for (int i = 0; get_piece(sched, p.kb, i, pc); ++i) {
-      const Unit u = find_unit<kTileM>(p, s_tiles, s_first, pc.unit);
-      const bool mine = quarter * 32 < u.rows;  // the warp has rows
-      const bool live = r < u.rows;
-      const size_t row = static_cast<size_t>(u.row0) + (live ? r : u.rows - 1);
-      const float* sx = p.sx + row * p.kb;
+    griddep_wait();
+    bool more = get_piece(sched, p.kb, 0, pc);
+    Unit u;
+    const float *sx, *sw0, *sw1;
+    float a_next, w0_next, w1_next;
+    auto begin = [&]() {  // the unit of pc, and its first scales on their way
+      u = find_unit<kTileM>(p, s_tiles, s_first, pc.unit);
+      sx = p.sx + static_cast<size_t>(u.row0 + min(r, u.rows - 1)) * p.kb;
       int n0 = GATED ? u.n : 2 * u.n + half;  // 128-row scale block of columns 0-63 of the half
       int n1 = GATED ? p.I / 128 + u.n : n0;  // and of columns 64-127
       n0 = min(n0, p.nb - 1);
       n1 = min(n1, p.nb - 1);
-      const float* sw0 = p.sw + (static_cast<size_t>(u.e) * p.nb + n0) * p.kb;
-      const float* sw1 = p.sw + (static_cast<size_t>(u.e) * p.nb + n1) * p.kb;
+      sw0 = p.sw + (static_cast<size_t>(u.e) * p.nb + n0) * p.kb;
+      sw1 = p.sw + (static_cast<size_t>(u.e) * p.nb + n1) * p.kb;
+      a_next = __ldg(sx + pc.k0);
+      w0_next = __ldg(sw0 + pc.k0);
+      w1_next = GATED ? __ldg(sw1 + pc.k0) : 0.0f;
+    };
+    if (more) begin();
+    for (int i = 0; more; ++i) {
+      const bool mine = quarter * 32 < u.rows;  // the warp has rows
+      const bool live = r < u.rows;
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
-      float a_next = __ldg(sx + pc.k0), w0_next = __ldg(sw0 + pc.k0), w1_next = GATED ? __ldg(sw1 + pc.k0) : 0.0f;
       for (int b = pc.k0; b < pc.k1; ++b, ++g) {
         const int t = g & 1;
         const float s0 = a_next * w0_next, s1 = GATED ? a_next * w1_next : s0;
@@ -538,20 +584,19 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           if (mine) {
             uint32_t v0[32], v1[32];
             const uint32_t ta = lane_addr + t * kAccCols;
+            // the stage is given back as soon as its last columns are in registers
             tmem_ld32(ta, v0);
-            tmem_wait(v0);
             tmem_ld32(ta + 32, v1);
+            tmem_wait2(v0, v1);
             fold32(acc, v0, s0);
-            tmem_wait(v1);
             tmem_ld32(ta + 64, v0);
             fold32(acc + 32, v1, s0);
-            tmem_wait(v0);
             tmem_ld32(ta + 96, v1);
-            fold32(acc + 64, v0, s1);
-            tmem_wait(v1);
+            tmem_wait2(v0, v1);
             k5::tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[t]);
+            fold32(acc + 64, v0, s1);
             fold32(acc + 96, v1, s1);
             continue;
           }
@@ -564,24 +609,29 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
 #pragma unroll
         for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
       }
-      if (pc.count > 1) {
+      const Piece done = pc;
+      const Unit du = u;
+      const size_t row = static_cast<size_t>(du.row0) + r;
+      more = get_piece(sched, p.kb, i + 1, pc);
+      if (more) begin();  // the next unit's loads pass while this one is written
+      if (done.count > 1) {
         // partial tile to the workspace; the last piece to arrive adds all of them in piece order
         const size_t slot_floats = static_cast<size_t>(kTileN) * p.rcap;
         if (live) {
-          float* d = p.part + pc.slot * slot_floats + static_cast<size_t>(half * 128) * p.rcap + r;
+          float* d = p.part + done.slot * slot_floats + static_cast<size_t>(half * 128) * p.rcap + r;
 #pragma unroll
           for (int c = 0; c < 128; ++c) __stcg(d + static_cast<size_t>(c) * p.rcap, acc[c]);
         }
-        if (!last_piece(p.counter + (pc.unit - sched.waves * static_cast<int>(gridDim.x)), pc.count, s_last))
+        if (!last_piece(p.counter + (done.unit - sched.waves * static_cast<int>(gridDim.x)), done.count, s_last))
           continue;
         if (live) {
-          const int j = pc.unit - sched.waves * static_cast<int>(gridDim.x);
+          const int j = done.unit - sched.waves * static_cast<int>(gridDim.x);
 #pragma unroll
           for (int c0 = 0; c0 < 128; c0 += 32) {
             float v[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-            for (int q = pc.first; q < pc.first + pc.count; ++q) {
+            for (int q = done.first; q < done.first + done.count; ++q) {
               const int slot = 2 * q + (piece_begin(sched, q) / p.kb == j ? 0 : 1);
               const float* d = p.part + slot * slot_floats + static_cast<size_t>(half * 128 + c0) * p.rcap + r;
 #pragma unroll
@@ -606,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
         const int ex = scale_exponent(m);
         const float inv = pow2(-ex);
         if (live) {
-          if (half == 0) p.hs[row * (p.I / 128) + u.n] = pow2(ex);
-          uint4* d = reinterpret_cast<uint4*>(p.hq + row * p.I + u.n * 128 + half * 64);
+          if (half == 0) p.hs[row * (p.I / 128) + du.n] = pow2(ex);
+          uint4* d = reinterpret_cast<uint4*>(p.hq + row * p.I + du.n * 128 + half * 64);
 #pragma unroll
           for (int c = 0; c < 64; c += 16) {
             uint32_t w[4];
@@ -619,8 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           }
         }
       } else if (mine) {
-        store_rows<TO>(smem + kOffStage + ew * 32 * kStageRow, p.y, static_cast<size_t>(u.row0) + quarter * 32,
-                       p.ld_y, min(32, u.rows - quarter * 32), u.n * kTileN + half * 128, p.N, p.vec, acc, lane);
+        store_rows<TO>(smem + kOffStage + ew * 32 * kStageRow, p.y, static_cast<size_t>(du.row0) + quarter * 32,
+                       p.ld_y, min(32, du.rows - quarter * 32), du.n * kTileN + half * 128, p.N, p.vec, acc, lane);
       }
     }
   }

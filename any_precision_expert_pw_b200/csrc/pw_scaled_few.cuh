@@ -109,8 +109,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  griddep_wait();
-  griddep_launch();
   k7::row_tiles<kTokens>(p, s_tiles, s_first);
   k5::tc_fence_before();
   __syncthreads();
@@ -126,28 +124,53 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     bool ok = true;
     if (warp == 0) {
       // ---------------- producer ----------------
+      // the first kStages weight tiles are on their way before the launch in front has ended; the
+      // tokens (its output) follow
+      auto tokens_of = [&](const Unit& u, int b, uint32_t stage) {
+        const uint32_t x = smem_base + stage * kStageBytes + kWBytes;
+        for (int q = 0; q * kBox < u.rows; ++q)
+          k7::tma_2d(x + q * kBox * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kBox, &full[stage]);
+      };
+      auto follow = [&]() {  // the tokens of the blocks before g
+        griddep_wait();
+        if (leader) {
+          uint32_t h = 0;
+          Piece q;
+          for (int i = 0; h < g && k7::get_piece(sched, p.kb, i, q); ++i) {
+            const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, q.unit);
+            for (int b = q.k0; b < q.k1 && h < g; ++b, ++h) tokens_of(u, b, h);
+          }
+          griddep_launch();
+        }
+        __syncwarp();
+      };
+      bool waited = false;
       for (int i = 0; ok && k7::get_piece(sched, p.kb, i, pc); ++i) {
         const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
         const int boxes = (u.rows + kBox - 1) / kBox;
         const uint32_t bytes = kWBytes + boxes * kBox * kBlk;
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
+          if (g == kStages && !waited) {
+            follow();
+            waited = true;
+          }
           const int s = g % kStages;
           if (!(ok = k7::warp_wait(&empty[s], ((g / kStages) & 1) ^ 1, abort_flag))) break;
           if (leader) {
             mbar_arrive_expect_tx(&full[s], bytes);
-            const uint32_t w = smem_base + s * kStageBytes, x = w + kWBytes;
+            const uint32_t w = smem_base + s * kStageBytes;
             if (GATED) {
               k7::tma_3d(w, &p.wmap, b * kBlk, u.n * 128, u.e, &full[s]);
               k7::tma_3d(w + kWBytes / 2, &p.wmap, b * kBlk, p.I + u.n * 128, u.e, &full[s]);
             } else {
               k7::tma_3d(w, &p.wmap, b * kBlk, u.n * kRows, u.e, &full[s]);
             }
-            for (int q = 0; q < boxes; ++q)
-              k7::tma_2d(x + q * kBox * kBlk, &p.xsmall, b * kBlk, u.row0 + q * kBox, &full[s]);
+            if (waited) tokens_of(u, b, s);
           }
           __syncwarp();
         }
       }
+      if (!waited) follow();
       // every issued copy has landed before the block exits
       if (leader)
         for (uint32_t x = (g > kStages ? g - kStages : 0); x < g; ++x)
@@ -191,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     uint32_t g = 0;
     Piece pc;
     bool dead = false;  // a wait gave up: keep every barrier, write zeros
+    griddep_wait();
     for (int i = 0; k7::get_piece(sched, p.kb, i, pc); ++i) {
       const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
       // lane l holds the scales of tokens l and l + 32

@@ -54,6 +54,36 @@ __device__ __forceinline__ void load_elems(const void* p, float (&v)[V]) {
   }
 }
 
+// The same V elements as they lie in memory (half the registers of fp32 for 16-bit types: what bounds
+// the row kernels is loads in flight), and their values.
+template <int TY, int V>
+struct Raw {
+  uint32_t w[V * ElemSize<TY>::value / 4 > 0 ? V * ElemSize<TY>::value / 4 : 1];
+};
+template <int TY, int V>
+__device__ __forceinline__ void load_raw(const void* p, Raw<TY, V>& r) {
+  constexpr int B = V * ElemSize<TY>::value;
+  static_assert(B == 2 || B == 4 || B == 16, "one load");
+  if constexpr (B == 16) {
+    const uint4 a = __ldg(static_cast<const uint4*>(p));
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+  } else if constexpr (B == 4) {
+    r.w[0] = __ldg(static_cast<const unsigned int*>(p));
+  } else {
+    r.w[0] = __ldg(static_cast<const unsigned short*>(p));
+  }
+}
+template <int TY, int V>
+__device__ __forceinline__ float raw_value(const Raw<TY, V>& r, int i) {
+  if constexpr (TY == PW_TYPE_F32) {
+    return __uint_as_float(r.w[i]);
+  } else if constexpr (TY == PW_TYPE_BF16) {
+    return __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+  } else {
+    return f16_to_f32(static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1))));
+  }
+}
+
 template <int TY>
 __device__ __forceinline__ uint16_t to_bits16(float f) {
   if constexpr (TY == PW_TYPE_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
@@ -116,6 +146,10 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 4;  // steps whose ids are loaded before the first is used
 
+// Warps that share a run of n slots: whole steps of 32 each, no more warps than steps (fewer rows of
+// the count table to clear and to sum).
+__device__ __forceinline__ int sort_warps(int n) { return min(kSortWarps, max(1, (n + 31) / 32)); }
+
 __device__ __forceinline__ int slot_expert(const int32_t* idx, int i, int end, int E) {
   if (i >= end) return -1;
   const int e = __ldg(idx + i);
@@ -155,18 +189,21 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t*
   extern __shared__ __align__(16) uint8_t sort_smem[];
   uint16_t* cnt = reinterpret_cast<uint16_t*>(sort_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) cnt[i] = 0;
-  __syncthreads();
-  griddep_wait();
   int a, b, wa, wb;
   run_of(n, gridDim.x, blockIdx.x, a, b);
-  run_of(b - a, kSortWarps, warp, wa, wb);
-  sort_count(idx, a + wa, a + wb, E, cnt + warp * E, lane);
+  const int warps = sort_warps(b - a);
+  for (int i = threadIdx.x; i < warps * E; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
+  griddep_wait();
   griddep_launch();
+  if (warp < warps) {
+    run_of(b - a, warps, warp, wa, wb);
+    sort_count(idx, a + wa, a + wb, E, cnt + warp * E, lane);
+  }
+  __syncthreads();
   for (int e = threadIdx.x; e < E; e += kSortThreads) {
     int s = 0;
-    for (int w = 0; w < kSortWarps; ++w) s += cnt[w * E + e];
+    for (int w = 0; w < warps; ++w) s += cnt[w * E + e];
     part[static_cast<size_t>(blockIdx.x) * E + e] = s;
   }
 }
@@ -201,26 +238,49 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
                                                                   int32_t* zero, int n_zero) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
   __shared__ int warp_sum[kSortWarps];
+  __shared__ int s_before[kSortThreads], s_all[kSortThreads];
   int* base = reinterpret_cast<int*>(sort_smem);                    // [E] first row of the CTA
   uint16_t* cnt = reinterpret_cast<uint16_t*>(base + E);            // [warps][E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) cnt[i] = 0;
+  int a, b, wa = 0, wb = 0;
+  run_of(n, gridDim.x, blockIdx.x, a, b);
+  const int warps = sort_warps(b - a);
+  for (int i = threadIdx.x; i < warps * E; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < n_zero; i += kSortThreads) zero[i] = 0;
-  int a, b, wa, wb;
-  run_of(n, gridDim.x, blockIdx.x, a, b);
-  run_of(b - a, kSortWarps, warp, wa, wb);
-  wa += a, wb += a;
-  sort_count(idx, wa, wb, E, cnt + warp * E, lane);
+  if (part) {
+    // counts of the CTAs before this one, and of all: `groups` threads an expert, each over its share
+    // of the CTAs
+    const int groups = kSortThreads / E, g = threadIdx.x / E, e = threadIdx.x - g * E;
+    int before = 0, all = 0;
+    if (g < groups) {
+      const int ctas = gridDim.x, me = blockIdx.x;
+      int c0, c1;
+      run_of(ctas, groups, g, c0, c1);
+#pragma unroll 8
+      for (int c = c0; c < c1; ++c) {
+        const int v = __ldcg(part + static_cast<size_t>(c) * E + e);
+        before += c < me ? v : 0;
+        all += v;
+      }
+    }
+    s_before[threadIdx.x] = before;
+    s_all[threadIdx.x] = all;
+  }
+  if (warp < warps) {
+    run_of(b - a, warps, warp, wa, wb);
+    wa += a, wb += a;
+    sort_count(idx, wa, wb, E, cnt + warp * E, lane);
+  }
   __syncthreads();
   // thread e: prefix over the warps; E <= 1024 = the block
   const int e = threadIdx.x;
   int run = 0;
   if (e < E)
-    for (int w = 0; w < kSortWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const int c = cnt[w * E + e];
       cnt[w * E + e] = static_cast<uint16_t>(run);
       run += c;
@@ -228,10 +288,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
   int before = 0, all = e < E ? run : 0;
   if (part && e < E) {
     all = 0;
-    for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-      const int v = __ldcg(part + static_cast<size_t>(c) * E + e);
-      before += c < static_cast<int>(blockIdx.x) ? v : 0;
-      all += v;
+    for (int g = 0; g < kSortThreads / E; ++g) {
+      before += s_before[g * E + e];
+      all += s_all[g * E + e];
     }
   }
   const int incl = block_inclusive(all, warp_sum);
@@ -332,7 +391,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const void* o, int T,
     for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
   constexpr int J = 4;
   for (int j0 = 0; j0 < k; j0 += J) {
-    float v[J][U][V];
+    Raw<TI, V> v[J][U];
     int r[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -341,8 +400,8 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const void* o, int T,
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (c0 + 32 * V * u < H)
-          load_elems<TI, V>(elem_at(o, static_cast<size_t>(r[j]) * ld_o + c0 + 32 * V * u,
-                                    ElemSize<TI>::value), v[j][u]);
+          load_raw<TI, V>(elem_at(o, static_cast<size_t>(r[j]) * ld_o + c0 + 32 * V * u,
+                                  ElemSize<TI>::value), v[j][u]);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -352,7 +411,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const void* o, int T,
       for (int u = 0; u < U; ++u)
         if (c0 + 32 * V * u < H) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[u][i] = fmaf(gj, v[j][u][i], acc[u][i]);
+          for (int i = 0; i < V; ++i) acc[u][i] = fmaf(gj, raw_value<TI, V>(v[j][u], i), acc[u][i]);
         }
     }
   }
@@ -375,6 +434,8 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(
   __shared__ int s_row[KM];
   __shared__ float s_gate[KM];
   __shared__ float s_sum[kGradThreads / 32][KM];
+  griddep_wait();
+  griddep_launch();
   const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int S = ElemSize<TY>::value;
   if (static_cast<int>(threadIdx.x) < KM) {
@@ -388,18 +449,18 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(
 #pragma unroll
   for (int j = 0; j < KM; ++j) acc[j] = 0.0f;
   for (int c = threadIdx.x * V; c < H; c += kGradThreads * V) {
-    float d[V];
-    load_elems<TY, V>(elem_at(dy, static_cast<size_t>(t) * ld_dy + c, S), d);
-    constexpr int J = 4;
+    Raw<TY, V> d;
+    load_raw<TY, V>(elem_at(dy, static_cast<size_t>(t) * ld_dy + c, S), d);
+    constexpr int J = 4;  // rows of o in flight (more cost occupancy)
 #pragma unroll
     for (int j0 = 0; j0 < KM; j0 += J) {
       if (j0 >= k) break;
-      float v[J][V];
+      Raw<TY, V> v[J];
       if (d_gate) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
           if (s_row[j0 + j] >= 0)
-            load_elems<TY, V>(elem_at(o, static_cast<size_t>(s_row[j0 + j]) * ld_o + c, S), v[j]);
+            load_raw<TY, V>(elem_at(o, static_cast<size_t>(s_row[j0 + j]) * ld_o + c, S), v[j]);
       }
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -407,12 +468,13 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(
         if (r < 0) continue;
         if (d_gate) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[j0 + j] = fmaf(d[i], v[j][i], acc[j0 + j]);
+          for (int i = 0; i < V; ++i)
+            acc[j0 + j] = fmaf(raw_value<TY, V>(d, i), raw_value<TY, V>(v[j], i), acc[j0 + j]);
         }
         if (d_o) {
           float w[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) w[i] = s_gate[j0 + j] * d[i];
+          for (int i = 0; i < V; ++i) w[i] = s_gate[j0 + j] * raw_value<TY, V>(d, i);
           store_elems<TY, V>(elem_at(d_o, static_cast<size_t>(r) * ld_do + c, S), w);
         }
       }

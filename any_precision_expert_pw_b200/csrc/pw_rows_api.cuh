@@ -27,7 +27,7 @@ inline bool vec_ok(const void* p, int size, int H, long long ld) {
 // A sort of n slots uses one CTA up to kSortOne (both measured: there a second launch costs more
 // than the longer walk), then one per kSortRun slots, at most one per SM.
 constexpr int kSortOne = 8192;
-constexpr int kSortRun = 4096;
+constexpr int kSortRun = 1024;
 int sort_ctas(int n, int sms) {
   if (n <= kSortOne) return 1;
   return std::min(sms, (n + kSortRun - 1) / kSortRun);
@@ -134,7 +134,7 @@ struct ScaledCall {
 
 // Rows per expert (on average over the experts that can have one) up to which the few-rows kernel
 // is used.
-constexpr int kFewRows = 48;
+constexpr int kFewRows = 32;
 
 int part_rows(int M) { return static_cast<int>(align_up(std::min(M, pw::k7::kTileM), 32)); }
 size_t part_bytes(int M) {
@@ -226,15 +226,18 @@ pw_status launch_combine_types(const void* o, int T, int k, int H, long long ld_
   constexpr int VI = 16 / pw::ElemSize<TI>::value;  // elements of one 16-byte load
   const bool vec = vec_ok(o, pw::ElemSize<TI>::value, H, ld_o) && aligned(y, 16) &&
                    ld_y * pw::ElemSize<TO>::value % 16 == 0;
-  constexpr int kCols = 256;  // columns of one warp
-  const int groups = (H + kCols - 1) / kCols;
+    // vectors (single elements) of a lane; 16-bit types take one of 8 (8192 x 8 rows of 3584 bf16: 41.6
+  // us, two 44.3), fp32 two of 4 (53.9 us, one 57.6)
+  constexpr int UV = 8 / VI, US = 8;
+  const int cols = vec ? 32 * UV * VI : 32 * US;  // columns of one warp
+  const int groups = (H + cols - 1) / cols;
   const long long grid = (static_cast<long long>(T) * groups + 7) / 8;
   if (grid > 0x7fffffffLL) return PW_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(256);
   if (vec)
-    return launch_dependent(pw::combine_rows_kernel<TI, TO, VI, 8 / VI>, g, b, 0, st, o, T, k, H,
+    return launch_dependent(pw::combine_rows_kernel<TI, TO, VI, UV>, g, b, 0, st, o, T, k, H,
                             static_cast<size_t>(ld_o), pos, gate, y, static_cast<size_t>(ld_y), groups);
-  return launch_dependent(pw::combine_rows_kernel<TI, TO, 1, 8>, g, b, 0, st, o, T, k, H,
+  return launch_dependent(pw::combine_rows_kernel<TI, TO, 1, US>, g, b, 0, st, o, T, k, H,
                           static_cast<size_t>(ld_o), pos, gate, y, static_cast<size_t>(ld_y), groups);
 }
 
@@ -263,10 +266,9 @@ pw_status launch_combine_grad(const void* dy, const void* o, int T, int k, int H
   auto kernel = k <= 4   ? pw::combine_grad_kernel<TY, V, 4>
                 : k <= 8 ? pw::combine_grad_kernel<TY, V, 8>
                          : pw::combine_grad_kernel<TY, V, 16>;
-  kernel<<<T, pw::kGradThreads, 0, st>>>(dy, o, T, k, H, static_cast<size_t>(ld_dy),
-                                         static_cast<size_t>(ld_o), pos, gate, d_o,
-                                         static_cast<size_t>(ld_do), d_gate);
-  return launch_status();
+  return launch_dependent(kernel, dim3(T), dim3(pw::kGradThreads), 0, st, dy, o, T, k, H,
+                          static_cast<size_t>(ld_dy), static_cast<size_t>(ld_o), pos, gate, d_o,
+                          static_cast<size_t>(ld_do), d_gate);
 }
 
 // Workspace of pw_moe_scaled_forward.

@@ -50,7 +50,11 @@ constexpr int kProducerRegs = 40, kEpilogueRegs = 232;
 constexpr int kSplitRegs = 128 * kProducerRegs + kEpiThreads * kEpilogueRegs;
 static_assert(kSplitRegs <= 65536, "register file");
 constexpr int kTmemCols = 512, kAccCols = 256;
-constexpr int kMinPiece = 4;  // K blocks: shorter pieces cost more in joining than they spread
+// Shortest piece, in K blocks: shorter ones cost more in joining than they spread.  (This kernel: 3001
+// ragged rows over 60 experts, K 2040, 81 us whole and 87 in pieces of 8; 64 rows x 5120 x 3584 24.5
+// us in pieces of 14 or more, 25.2 of 9, 34.7 of 4.  The few-rows kernel: 16 rows 16.5 us in pieces of
+// 9, 18.6 of 14.)
+constexpr int kMinPiece = 12;
 
 constexpr int kOffBar = kStages * kStageBytes;
 constexpr int kNumBars = 2 * kStages + 4 + 1;
@@ -85,20 +89,17 @@ struct alignas(64) Params {
 struct Sched {
   int units, waves, rem, pieces, run;  // run: K blocks of the remainder, cut into `pieces`
 };
-// EVEN: the remainder is cut into equal runs over all CTAs, wherever units end (joins are cheap: few
-// rows).  Otherwise every unit of it is cut into the same number of pieces, so that a unit has the
-// fewest pieces to join and none is cut for less than its share of a whole CTA.
-template <bool EVEN>
-__device__ __forceinline__ Sched make_sched(int units, int kb, int grid) {
+// The units behind the last whole wave are cut while CTAs would stay without one: every such unit
+// into the same number of pieces, so that a unit has the fewest pieces to join.  (Cutting them into
+// equal runs for all CTAs, wherever a unit ends, costs more in joins than it spreads: 4 tokens x
+// 28672 x 4096, 112 units, 34.6 us against 29.0 with 112 CTAs at work; 112 SMs draw what HBM gives.)
+__device__ __forceinline__ Sched make_sched(int units, int kb, int grid, int min_piece) {
   Sched s;
   s.units = units;
   s.waves = units / grid;
   s.rem = units - s.waves * grid;
   s.run = s.rem * kb;
-  if (EVEN)
-    s.pieces = min(grid, max(s.rem, s.run / kMinPiece));
-  else
-    s.pieces = s.rem ? s.rem * max(1, min(grid / s.rem, kb / kMinPiece)) : 0;
+  s.pieces = s.rem ? s.rem * max(1, min(grid / s.rem, kb / min_piece)) : 0;
   return s;
 }
 __device__ __forceinline__ int piece_begin(const Sched& s, int p) {
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
   __syncthreads();
   k5::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const Sched sched = make_sched<false>(s_tiles[E] * p.nt, p.kb, gridDim.x);
+  const Sched sched = make_sched(s_tiles[E] * p.nt, p.kb, gridDim.x, kMinPiece);
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp < 4) {
@@ -626,19 +627,28 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           continue;
         if (live) {
           const int j = done.unit - sched.waves * static_cast<int>(gridDim.x);
+          auto piece_at = [&](int q) {
+            const int slot = 2 * q + (piece_begin(sched, q) / p.kb == j ? 0 : 1);
+            return p.part + slot * slot_floats + static_cast<size_t>(half * 128) * p.rcap + r;
+          };
+          if (done.count == 2) {  // the other piece onto this one, in registers: the order is no matter
+            const float* d = piece_at(2 * done.first + 1 - static_cast<int>(blockIdx.x));
 #pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            float v[32];
+            for (int c = 0; c < 128; ++c) acc[c] += __ldcg(d + static_cast<size_t>(c) * p.rcap);
+          } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-            for (int q = done.first; q < done.first + done.count; ++q) {
-              const int slot = 2 * q + (piece_begin(sched, q) / p.kb == j ? 0 : 1);
-              const float* d = p.part + slot * slot_floats + static_cast<size_t>(half * 128 + c0) * p.rcap + r;
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+              float v[32];
 #pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] += __ldcg(d + static_cast<size_t>(c) * p.rcap);
+              for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+              for (int q = done.first; q < done.first + done.count; ++q) {
+                const float* d = piece_at(q) + static_cast<size_t>(c0) * p.rcap;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] += __ldcg(d + static_cast<size_t>(c) * p.rcap);
+              }
+#pragma unroll
+              for (int c = 0; c < 32; ++c) acc[c0 + c] = v[c];
             }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) acc[c0 + c] = v[c];
           }
         }
       }

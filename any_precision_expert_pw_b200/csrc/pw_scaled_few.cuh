@@ -29,6 +29,7 @@ constexpr int kStages = 5;
 constexpr int kWBytes = kRows * kBlk, kXBytes = kTokens * kBlk;
 constexpr int kStageBytes = kWBytes + kXBytes;
 constexpr int kThreads = 384, kEpiThreads = 256;
+constexpr int kMinPiece = 8;                        // K blocks of the shortest piece (see k7::kMinPiece)
 constexpr int kAccStages = 4;                       // K blocks in tensor memory
 constexpr int kTmemCols = kAccStages * 2 * kTokens;  // 512
 constexpr int kBox = k7::kSmallRows;                // tokens of an activation box, and of an MMA's step of N
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   __syncthreads();
   k5::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const Sched sched = k7::make_sched<true>(s_tiles[E] * p.nt, p.kb, gridDim.x);
+  const Sched sched = k7::make_sched(s_tiles[E] * p.nt, p.kb, gridDim.x, kMinPiece);
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp < 2) {

@@ -528,61 +528,111 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return r;
 }
 
-// One half-warp per (row, 128-column block): 8 columns a lane.  pos == NULL: to row t of q; else to
-// the rows of the token's k slots (quantise and dispatch in one pass).  Bound by the bytes.
-template <int TY, bool VEC>
+// Four values to a word of e4m3, |v| <= 448 or NaN.
+__device__ __forceinline__ uint32_t e4m3_word(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// One half-warp per (row, 128-column block), 8 columns a lane, U rows in flight; a CTA's sixteen
+// half-warps take up to 16 blocks of a row (blockIdx.y: the next 16), and rp rows side by side where a
+// row has fewer.  pos == NULL: to row t of q; else to the rows of the token's k slots (quantise and
+// dispatch in one pass).  Bound by the bytes.
+template <int TY, bool VEC, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, long long rows, int cols,
                                                             size_t ld_x, int k, const int32_t* pos,
                                                             uint8_t* q, size_t ld_q, float* scale,
                                                             int blocks) {
   constexpr int S = ElemSize<TY>::value;
-  const int lane = threadIdx.x & 31, sub = lane & 15;
+  const int lane = threadIdx.x & 31, sub = lane & 15, hw = threadIdx.x >> 4;
   griddep_wait();
   griddep_launch();
-  const long long unit = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 2 + (lane >> 4);
-  const long long t = unit / blocks;
-  const int b = static_cast<int>(unit - t * blocks);
-  const int c = b * 128 + sub * 8;
-  const bool in = t < rows;
-  float v[8];
+  const int nb = min(16, blocks), rp = 16 / nb, r_in = hw / nb;
+  const int b = blockIdx.y * 16 + hw - r_in * nb, c = b * 128 + sub * 8;
+  const long long t0 = static_cast<long long>(blockIdx.x) * rp * U + r_in;
+  const bool in = r_in < rp && b < blocks;
+  // The loads of all U rows first, without a branch (a lane beyond the matrix repeats its last values
+  // and counts for nothing below).  What the integer pipe does per value decides the time of this
+  // kernel, so values stay packed as long as they can.
+  constexpr int W = TY == PW_TYPE_F32 ? 4 : 8;  // elements of 16 bytes
+  Raw<TY, W> raw[U][8 / W];
+  const int cc = min(c, cols - 8);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (in) {
-    if (VEC) {  // cols % 8 == 0
-      if (c < cols) load_elems<TY, 8>(elem_at(x, static_cast<size_t>(t) * ld_x + c, S), v);
-    } else {
+  for (int u = 0; u < U; ++u) {
+    const long long t = min(t0 + u * rp, rows - 1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < cols) {
-          float one[1];
-          load_elems<TY, 1>(elem_at(x, static_cast<size_t>(t) * ld_x + c + i, S), one);
-          v[i] = one[0];
-        }
+    for (int i = 0; i < 8 / W; ++i) {
+      if (VEC) {  // cols % 8 == 0
+        load_raw<TY, W>(elem_at(x, static_cast<size_t>(t) * ld_x + cc + i * W, S), raw[u][i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw[u][i].w[j] = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (c + i * W + j < cols) {
+            Raw<TY, 1> one;
+            load_raw<TY, 1>(elem_at(x, static_cast<size_t>(t) * ld_x + c + i * W + j, S), one);
+            if (TY == PW_TYPE_F32) raw[u][i].w[j & 3] = one.w[0];
+            else raw[u][i].w[j / 2] |= one.w[0] << (16 * (j & 1));
+          }
+      }
     }
   }
-  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
+  for (int u = 0; u < U; ++u) {
+    const long long t = t0 + u * rp;
+    const bool here = in && t < rows;
+    // rows of the token's slots, one a lane (k <= 16)
+    int row = -1;
+    if (pos && here && sub < k) row = checked_row(pos, t * k + sub, static_cast<int>(rows * k));
+    // largest magnitude by its bits: infinities and NaN come out on top and are looked at apart
+    uint32_t top = 0;
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  const int e = scale_exponent(m);
-  const float inv = pow2(-e);
-  const uint32_t w0 = e4m3_pair(v[0] * inv, v[1] * inv) | (e4m3_pair(v[2] * inv, v[3] * inv) << 16);
-  const uint32_t w1 = e4m3_pair(v[4] * inv, v[5] * inv) | (e4m3_pair(v[6] * inv, v[7] * inv) << 16);
-  const uint2 w = make_uint2(w0, w1);
-  if (!in) return;
-  const int slots = pos ? k : 1;
-  for (int j = 0; j < slots; ++j) {
-    const long long r = pos ? checked_row(pos, t * k + j, static_cast<int>(rows * k)) : t;
-    if (r < 0) continue;
-    if (sub == 0) scale[r * blocks + b] = pow2(e);
-    uint8_t* d = q + static_cast<size_t>(r) * ld_q + c;
-    if (c + 8 <= cols) {
-      *reinterpret_cast<uint2*>(d) = w;
-    } else {
+    for (int i = 0; i < 8 / W; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < cols) d[i] = static_cast<uint8_t>((i < 4 ? w0 >> (8 * i) : w1 >> (8 * (i - 4))) & 0xffu);
+      for (int j = 0; j < 4; ++j)
+        top = TY == PW_TYPE_F32 ? max(top, raw[u][i].w[j] & 0x7fffffffu)
+                                : __vmaxu2(top, raw[u][i].w[j] & 0x7fff7fffu);
+    if (!here || c >= cols) top = 0;
+    if (TY != PW_TYPE_F32) top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (TY == PW_TYPE_BF16) top <<= 16;
+    if (TY == PW_TYPE_F16) top = __float_as_uint(f16_to_f32(static_cast<uint16_t>(top)));
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = raw_value<TY, W>(raw[u][i / W], i % W);
+    if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m = fmaxf(m, finite_abs(v[i]));
+        if (fabsf(v[i]) > 3.402823466e38f) v[i] = __uint_as_float(0x7fffffffu);  // NaN
+      }
+      if (!here || c >= cols) m = 0.0f;
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      top = __float_as_uint(m);
+    }
+    const int e = scale_exponent(__uint_as_float(top));
+    const float inv = pow2(-e);
+    const uint32_t w0 = e4m3_word(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    const uint32_t w1 = e4m3_word(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    const int slots = pos ? k : 1;
+    for (int j = 0; j < slots; ++j) {
+      const long long r = pos ? __shfl_sync(0xffffffffu, row, (lane & 16) + j) : (here ? t : -1);
+      if (r < 0) continue;
+      if (sub == 0) scale[r * blocks + b] = pow2(e);
+      uint8_t* d = q + static_cast<size_t>(r) * ld_q + c;
+      if (VEC ? c < cols : c + 8 <= cols) {
+        *reinterpret_cast<uint2*>(d) = make_uint2(w0, w1);
+      } else if (!VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) d[i] = static_cast<uint8_t>((i < 4 ? w0 >> (8 * i) : w1 >> (8 * (i - 4))) & 0xffu);
+      }
     }
   }
 }

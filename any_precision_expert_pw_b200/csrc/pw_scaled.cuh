@@ -44,9 +44,9 @@ constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kSmallRows = 16;  // rows of the small activation box
 constexpr int kThreads = 384;
 constexpr int kEpiThreads = 256;
-// registers a thread: 40 in the producer warpgroup, 232 in the two epilogue warpgroups (128
+// registers a thread: 56 in the producer warpgroup, 224 in the two epilogue warpgroups (128
 // accumulators and two buffers of 32); their sum may not exceed what the block is launched with
-constexpr int kProducerRegs = 40, kEpilogueRegs = 232;
+constexpr int kProducerRegs = 56, kEpilogueRegs = 224;
 constexpr int kSplitRegs = 128 * kProducerRegs + kEpiThreads * kEpilogueRegs;
 static_assert(kSplitRegs <= 65536, "register file");
 constexpr int kTmemCols = 512, kAccCols = 256;
@@ -210,6 +210,15 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 // split warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+}
+
+// Both barriers, for the warp that feeds the tensor cores: the two tries run together and one vote
+// serves both (a block's turn of that warp has to stay under the block's 512 cycles of products).
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           volatile int* abort_flag) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  if (__all_sync(0xffffffffu, ra && rb)) return true;
+  return __all_sync(0xffffffffu, wait_bar(a, pa, abort_flag) && wait_bar(b, pb, abort_flag));
 }
 
 // ---- tcgen05 / TMA ----
@@ -510,27 +519,28 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           mbar_wait(&full[x % kStages], (x / kStages) & 1);
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
+      const uint64_t ad0 = sw128_desc(smem_base);
       uint32_t g = 0;
       Piece pc;
       bool ok = true;
       for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
           const int s = g % kStages, t = g & 1;
-          if (!(ok = warp_wait(&full[s], (g / kStages) & 1, abort_flag))) break;
-          const uint64_t ad = sw128_desc(smem_base + s * kStageBytes);
-          const uint64_t bd = sw128_desc(smem_base + s * kStageBytes + kABytes);
-          if (!(ok = warp_wait(&acc_empty[t], ((g >> 1) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = warp_wait2(&full[s], (g / kStages) & 1, &acc_empty[t], ((g >> 1) & 1) ^ 1, abort_flag)))
+            break;
           k5::tc_fence_after();
+          const uint64_t ad = ad0 + static_cast<uint64_t>(s) * (kStageBytes / 16);
+          const uint32_t d = tmem_base + t * kAccCols;
           if (leader) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)  // 32 bytes of K each
-              mma_f8(tmem_base + t * kAccCols, ad + 2 * j, bd + 2 * j, kInstr, j > 0);
-            k5::mma_commit(&empty[s]);
+              mma_f8(d, ad + 2 * j, ad + kABytes / 16 + 2 * j, kInstr, j > 0);
             k5::mma_commit(&acc_full[t]);
+            k5::mma_commit(&empty[s]);
           }
-          __syncwarp();
         }
       }
+      __syncwarp();
       if (leader) {
         k5::mma_commit(mma_done);
         mbar_wait(mma_done, 0);

@@ -10,11 +10,17 @@
 // the next product (one power-of-two scale per row and 128 features: one tile).
 //
 // Work: units of 128 rows x 256 columns (gated: 128 gate and the 128 matching up columns), in order
-// of expert, column tile, row tile; one CTA per SM.  Whole waves of units go one unit to a CTA.  The
-// rest (U mod SMs units) is cut along K into equal runs of K blocks, one per CTA, so a decode step
-// with few units still streams weights on every SM; a unit cut into pieces is joined by the CTA that
-// finishes last (partials and a counter in the workspace; the sum runs in piece order whoever joins,
-// so results repeat bit for bit).  Nobody waits for another CTA.
+// of expert, column tile, row tile; one CTA per SM.  Whole waves of units go one unit to a CTA.  Where
+// the rest (U mod SMs units) would leave CTAs idle each of its units is cut along K into pieces, one
+// per CTA, and joined by the CTA that finishes last (partials and a counter in the workspace; the sum
+// runs in piece order whoever joins, so results repeat bit for bit).  Nobody waits for another CTA.
+//
+// What bounds it: per SM and block the products take 512 cycles, and two blocks (2 x 256 columns) are
+// all that tensor memory holds, so a block's turn is half of products + signals + reading back:
+// about 875 cycles (4736 x 1024, one unit an SM: 0.55 us a block at the 1.6 GHz seen under this load,
+// 2.0 PFLOP/s; 4096 x 5120 x 3584: 88 us, 1.7 PFLOP/s).  Tried and slower: 128-column products
+// with four half stages (rows read twice from shared memory), sixteen epilogue warps of 64
+// columns, scales loaded two blocks ahead (registers).
 //
 // Order of launches: a launch before the one in front of this one has completed when this one starts
 // (every kernel here lets its dependents start only after its own wait), so the offsets and the
@@ -184,8 +190,8 @@ __device__ __forceinline__ Unit find_unit(const Params& p, const int* tiles, con
 // ---- waits ----
 // Bounded wait on an mbarrier, as mbar_wait, but the clock and the limit (a global load) are read
 // only after several suspended tries: this kernel hands tensor-memory stages back and forth every
-// few hundred cycles, and a wait that reads the limit first costs more than a stage takes (M 4736,
-// N 1024, K 16384: 98.9 us with mbar_wait, 88.8 us so).
+// few hundred cycles, and a wait that reads the limit first costs more than a stage takes (4736 x
+// 1024 x 16384: 98.9 us with mbar_wait, 88.8 us so).
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const unsigned long long t0 = global_ns();
   const unsigned long long limit = wait_limit_ns();
@@ -519,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           mbar_wait(&full[x % kStages], (x / kStages) & 1);
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
+      griddep_wait();  // nothing to multiply before; the bounded waits below start after it
       const uint64_t ad0 = sw128_desc(smem_base);
       uint32_t g = 0;
       Piece pc;

@@ -3,7 +3,10 @@
 // weight rows x 64 tokens; gated: 128 gate rows and the 128 matching up rows) wastes nothing on rows
 // that do not exist, a lane of tensor memory is a feature, and partials, joins and outputs are
 // contiguous across lanes.  What bounds it is the weights' bytes, each read once: 5 stages of 32 KB
-// keep 160 KB a SM in flight, and the schedule cuts the last wave of units along K into equal runs.
+// keep 160 KB an SM in flight.  64 experts of 8 rows, 5120 x 3584: 185 us, 6.4 TB/s; 4 rows x 28672 x
+// 4096 (117 MB): 24 us, of which about 5 until the first tile is there and what is left at the end.
+// From 64 rows an expert on the large-rows kernel is as fast or faster (64 x 28672 x 4096: 34.2 us
+// here, 31.1 there; 64 experts of 32 rows: 202 here, 206 there).
 //
 // A block's scale of a token is a column's here: the epilogue multiplies it with the weights' scale
 // once per (token, block) and reads it back from shared memory as it folds.
@@ -178,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
           mbar_wait(&full[x % kStages], (x / kStages) & 1);
     } else {
       // ---------------- MMA issuer ----------------
+      griddep_wait();  // nothing to multiply before; the bounded waits below start after it
       for (int i = 0; ok && k7::get_piece(sched, p.kb, i, pc); ++i) {
         const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
         const uint32_t id = instr((u.rows + kBox - 1) / kBox * kBox);

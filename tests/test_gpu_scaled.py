@@ -106,9 +106,11 @@ def check(y, y_name, xv, v, off, K):
     assert (got[n:] == -77.0).all() and y.outside_untouched()
 
 
-DENSE = [(1, 1, 1), (1, 128, 128), (4, 256, 128), (3, 300, 200), (17, 129, 136), (64, 512, 4096),
-         (65, 255, 1111), (128, 256, 256), (129, 257, 640), (300, 700, 384), (1, 40000, 256),
-         (2, 1000, 8192), (700, 9000, 128)]
+# both kernels (up to 32 rows an expert, and above), whole units and units cut into two and more pieces,
+# more units than SMs, sizes that end inside a block, a row tile or a 16-row box
+DENSE = [(1, 1, 1), (1, 128, 128), (4, 256, 128), (3, 300, 200), (17, 129, 136), (32, 300, 520),
+         (33, 300, 520), (64, 512, 4096), (65, 255, 1111), (128, 256, 256), (129, 257, 640),
+         (256, 512, 8192), (300, 700, 384), (1, 40000, 256), (2, 1000, 8192), (700, 9000, 128)]
 
 
 @pytest.mark.parametrize("y_name", list(TYPES))
@@ -121,7 +123,8 @@ def test_product_dense(libpw, M, N, K, y_name):
 
 
 GROUPED = [([0, 3], 256, 128), ([0, 0, 5, 5, 6], 300, 264), ([0, 1, 2, 3, 4, 5, 6, 7, 8], 384, 512),
-           ([0, 130, 130, 131, 400], 520, 384), ([0, 0, 0], 256, 128), ([0, 200, 260], 8192, 256)]
+           ([0, 130, 130, 131, 400], 520, 384), ([0, 0, 0], 256, 128), ([0, 200, 260], 8192, 256),
+           ([0, 90, 91, 91, 95], 300, 384), ([0, 0, 64, 128, 129], 130, 3000)]
 
 
 @pytest.mark.parametrize("off,N,K", GROUPED)
@@ -204,6 +207,7 @@ def _layer(H, I, E, seed):
 
 
 LAYERS = [(1, 2, 8, 256, 512, "f32", "f32"), (4, 2, 8, 256, 512, "bf16", "f32"), (33, 4, 12, 128, 384, "bf16", "bf16"),
+          (150, 1, 1, 4096, 128, "bf16", "f32"), (8, 1, 1, 4096, 256, "bf16", "f32"), (2, 1, 3, 128, 4096, "f16", "f32"),
           (1, 1, 1, 128, 128, "f16", "f16"), (70, 3, 5, 384, 128, "f32", "bf16"), (300, 2, 3, 256, 256, "bf16", "f32")]
 
 
@@ -333,3 +337,72 @@ def test_quantized_weights_object(libpw):
     ref, tol = moe_bound(x.double().cpu().numpy(), idx, gate, np.stack(v[0]), np.stack(v[1]))
     assert (np.abs(y - ref) <= tol + U * np.abs(ref)).all()
     assert B.pw_get_status() == B.PW_OK
+
+
+def test_layer_without_any_assignment(libpw):
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    tensors, _, _ = _layer(128, 128, 4, 19)
+    ex = ScaledExperts(*tensors, max_tokens=70, k=2)
+    ex.workspace.fill_(0xFF)
+    for T in (1, 70):
+        y = torch.full((T, 128), -7.0, device="cuda")
+        ex.forward(torch.randn(T, 128, device="cuda"), torch.full((T, 2), -1, dtype=torch.int32, device="cuda"),
+                   torch.full((T, 2), float("nan"), device="cuda"), y)
+        assert B.pw_get_status() == B.PW_OK and bool((y == 0).all())
+
+
+@pytest.mark.parametrize("T,E", [(3, 8), (200, 2)])
+def test_layer_stays_inside_its_buffers(libpw, T, E):
+    import torch
+    H, I, k = 256, 384, 2
+    (q1, s1, q2, s2), _, _ = _layer(H, I, E, 20)
+    st = B.pw_scaled_experts(E=E, H=H, I=I, gate_up=q1.data_ptr(), gate_up_scale=s1.data_ptr(),
+                             down=q2.data_ptr(), down_scale=s2.data_ptr())
+    x = torch.randn(T, H, device="cuda")
+    idx, gate = gpu(routing(T, E, k, 21)), torch.rand(T, k, device="cuda")
+    y = torch.full((T + 64, H), -77.0, device="cuda")
+    n = B.pw_moe_scaled_workspace_bytes(T, k, E, H, I)
+    ws = torch.full((n + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    B.check(B.pw_moe_scaled_forward(st, x.data_ptr(), B.PW_TYPE_F32, T, k, idx.data_ptr(), gate.data_ptr(),
+                                    y[32:].data_ptr(), B.PW_TYPE_F32, ws.data_ptr(), n))
+    assert B.pw_get_status() == B.PW_OK
+    assert bool((ws[n:] == 0xA5).all()) and bool((y[:32] == -77.0).all()) and bool((y[32 + T:] == -77.0).all())
+    assert bool(y[32:32 + T].isfinite().all())
+
+
+def test_gradient_on_transposed_blocks(libpw):
+    """d_x = d_y W: square blocks transpose with their scales, so it is the product on W^T."""
+    rng = np.random.default_rng(22)
+    N, K, M = 300, 200, 40
+    q, s, v = weights(1, N, K, 23)
+    qt, st = np.ascontiguousarray(q.transpose(0, 2, 1)), np.ascontiguousarray(s.transpose(0, 2, 1))
+    y, dyv = product(rng.normal(size=(M, N)), qt, st, None, K, "f32")
+    ref = dyv @ v[0]
+    mag = np.abs(dyv) @ np.abs(v[0])
+    assert (np.abs(y.np() - ref) <= (sum_bound(-(-N // 128)) + U) * mag).all()
+
+
+def test_products_beyond_32_bits(libpw):
+    """Rows whose offsets pass 2^32 elements: the first, a middle one and the last against the oracle."""
+    import torch
+    M, N, K = 280000, 130, 16384
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_()
+    xq = torch.empty(M, K, dtype=torch.uint8, device="cuda")
+    xs = torch.empty(M, K // 128, device="cuda")
+    B.check(B.pw_scaled_quantize(x.data_ptr(), B.PW_TYPE_BF16, M, K, K, 1, xq.data_ptr(), K, xs.data_ptr()))
+    q, s, v = weights(1, N, K, 24)
+    w, ldw = padded_codes(q)
+    ws = gpu(s)
+    n = B.pw_scaled_gemm_workspace_bytes(M, N, K, 1)
+    tmp = torch.empty(n, dtype=torch.uint8, device="cuda")
+    y = torch.empty(M, 16400, device="cuda")                # rows 16400 apart: 2^32 elements too
+    B.check(B.pw_scaled_gemm(xq.data_ptr(), xs.data_ptr(), M, K, K, w.data_ptr(), ws.data_ptr(), 1, N, ldw, 0,
+                             y.data_ptr(), B.PW_TYPE_F32, 16400, tmp.data_ptr(), n))
+    assert B.pw_get_status() == B.PW_OK
+    pick = [0, 1, M // 2, M - 2, M - 1]
+    xv = S.values(*S.quantize(x[pick].double().cpu().numpy(), 1), 1)
+    ref, mag = xv @ v[0].T, np.abs(xv) @ np.abs(v[0]).T
+    assert (np.abs(y[pick][:, :N].double().cpu().numpy() - ref) <= (sum_bound(K // 128) + U) * mag).all()

@@ -70,6 +70,30 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// The i-th piece of a CTA: its piece of the remainder first (within one unit: pieces >= rem), then its
+// units of the whole waves, so that a join is not what the launch ends with (64 tokens through 64
+// experts 295 us, last 301).  One workspace slot a CTA.
+__device__ __forceinline__ bool piece_first(const Sched& s, int kb, int i, Piece& p) {
+  const int cta = blockIdx.x;
+  const bool extra = cta < s.pieces;  // pieces = 0 without a remainder
+  p.first = 0;
+  p.count = 1;
+  if (extra && i == 0) {
+    const int a = k7::piece_begin(s, cta), j = a / kb;
+    p.unit = s.waves * static_cast<int>(gridDim.x) + j;
+    p.k0 = a - j * kb;
+    p.k1 = min(kb, k7::piece_begin(s, cta + 1) - j * kb);
+    p.first = k7::piece_of(s, j * kb);
+    p.count = k7::piece_of(s, (j + 1) * kb - 1) - p.first + 1;
+    return true;
+  }
+  const int w = extra ? i - 1 : i;
+  p.unit = cta + w * static_cast<int>(gridDim.x);
+  p.k0 = 0;
+  p.k1 = kb;
+  return w < s.waves;
+}
+
 template <bool GATED, int TO>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Params p) {
   uint8_t* const smem = k4::g_smem;
@@ -140,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (leader) {
           uint32_t h = 0;
           Piece q;
-          for (int i = 0; h < g && k7::get_piece(sched, p.kb, i, q); ++i) {
+          for (int i = 0; h < g && piece_first(sched, p.kb, i, q); ++i) {
             const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, q.unit);
             for (int b = q.k0; b < q.k1 && h < g; ++b, ++h) tokens_of(u, b, h);
           }
@@ -149,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         __syncwarp();
       };
       bool waited = false;
-      for (int i = 0; ok && k7::get_piece(sched, p.kb, i, pc); ++i) {
+      for (int i = 0; ok && piece_first(sched, p.kb, i, pc); ++i) {
         const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
         const int boxes = (u.rows + kBox - 1) / kBox;
         const uint32_t bytes = kWBytes + boxes * kBox * kBlk;
@@ -182,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     } else {
       // ---------------- MMA issuer ----------------
       griddep_wait();  // nothing to multiply before; the bounded waits below start after it
-      for (int i = 0; ok && k7::get_piece(sched, p.kb, i, pc); ++i) {
+      for (int i = 0; ok && piece_first(sched, p.kb, i, pc); ++i) {
         const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
         const uint32_t id = instr((u.rows + kBox - 1) / kBox * kBox);
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
@@ -220,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     Piece pc;
     bool dead = false;  // a wait gave up: keep every barrier, write zeros
     griddep_wait();
-    for (int i = 0; k7::get_piece(sched, p.kb, i, pc); ++i) {
+    for (int i = 0; piece_first(sched, p.kb, i, pc); ++i) {
       const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
       // lane l holds the scales of tokens l and l + 32
       const float* sx0 = p.sx + (static_cast<size_t>(u.row0) + min(lane, u.rows - 1)) * p.kb;
@@ -273,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       if (pc.count > 1) {
         // partials to the workspace, [token][256]; the last piece to arrive adds all in piece order
         const size_t slot_floats = static_cast<size_t>(kRows) * p.rcap;
-        float* d = p.part + pc.slot * slot_floats + half * 128 + f;
+        float* d = p.part + blockIdx.x * slot_floats + half * 128 + f;
 #pragma unroll
         for (int c = 0; c < kTokens; ++c)
           if (c < u.rows) __stcg(d + c * kRows, acc[c]);
@@ -290,8 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
               for (int q = 0; q < Q; ++q) {
                 const bool in = q0 + q < pc.first + pc.count;
-                const int slot = 2 * (q0 + q) + (in && k7::piece_begin(sched, q0 + q) / p.kb != j ? 1 : 0);
-                const float* src = p.part + slot * slot_floats + half * 128 + f;
+                const float* src = p.part + (q0 + q) * slot_floats + half * 128 + f;
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                   v[q][c] = in && c0 + c < u.rows ? __ldcg(src + (c0 + c) * kRows) : 0.0f;

@@ -194,6 +194,8 @@ pw_status launch_sort(const int32_t* idx, int T, int k, int E, int32_t* pos, int
                       cudaStream_t st) {
   const int n = T * k, ctas = sort_ctas(n, std::min(sms, kScaledMaxGrid));
   const dim3 block(pw::kSortThreads);
+  // a warp counts its part in 16 bits (148 CTAs: 3543 slots at most)
+  if (n / ctas / pw::kSortWarps >= 65535) return PW_ERR_UNSUPPORTED;
   if (ctas > 1 &&
       launch_dependent(pw::sort_count_kernel, dim3(ctas), block,
                        2 * pw::kSortWarps * static_cast<size_t>(E), st, idx, n, E, part) != PW_OK)

@@ -40,8 +40,8 @@ constexpr int kBox = k7::kSmallRows;                // tokens of an activation b
 constexpr int kOffBar = kStages * kStageBytes;
 constexpr int kNumBars = 2 * kStages + 2 * kAccStages + 1;
 constexpr int kOffMisc = kOffBar + ((kNumBars * 8 + 15) / 16) * 16;
-constexpr int kOffScale = kOffMisc + 32;                     // [8 warps][64] scales of the block
-constexpr int kOffEx = kOffScale + 8 * kTokens * 4;          // [16][128] exchange of 16 tokens
+constexpr int kOffScale = kOffMisc + 32;                     // [8 warps][2][64] scales of a block
+constexpr int kOffEx = kOffScale + 8 * 2 * kTokens * 4;      // [16][128] exchange of 16 tokens
 constexpr int kOffTiles = kOffEx + kBox * 128 * 4;
 constexpr int smem_bytes(int E) { return kOffTiles + 2 * (E + 1) * 4; }
 static_assert(smem_bytes(PW_MAX_EXPERTS) <= 227 * 1024, "shared memory budget");
@@ -206,29 +206,31 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     } else {
       // ---------------- MMA issuer ----------------
       griddep_wait();  // nothing to multiply before; the bounded waits below start after it
+      const uint64_t wd0 = k7::sw128_desc(smem_base);
       for (int i = 0; ok && piece_first(sched, p.kb, i, pc); ++i) {
         const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
         const uint32_t id = instr((u.rows + kBox - 1) / kBox * kBox);
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
           const int s = g % kStages, t = g % kAccStages;
-          if (!(ok = k7::warp_wait(&acc_empty[t], ((g / kAccStages) & 1) ^ 1, abort_flag))) break;
-          if (!(ok = k7::warp_wait(&full[s], (g / kStages) & 1, abort_flag))) break;
+          if (!(ok = k7::warp_wait2(&full[s], (g / kStages) & 1, &acc_empty[t], ((g / kAccStages) & 1) ^ 1,
+                                    abort_flag)))
+            break;
           k5::tc_fence_after();
-          const uint64_t wd = k7::sw128_desc(smem_base + s * kStageBytes);
-          const uint64_t xd = k7::sw128_desc(smem_base + s * kStageBytes + kWBytes);
+          const uint64_t wd = wd0 + static_cast<uint64_t>(s) * (kStageBytes / 16);
           const uint32_t d = tmem_base + t * 2 * kTokens;
           if (leader) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int j = 0; j < 4; ++j)  // 32 bytes of K each
-                k7::mma_f8(d + h * kTokens, wd + h * (kWBytes / 2 / 16) + 2 * j, xd + 2 * j, id, j > 0);
-            k5::mma_commit(&empty[s]);
+                k7::mma_f8(d + h * kTokens, wd + h * (kWBytes / 2 / 16) + 2 * j, wd + kWBytes / 16 + 2 * j, id,
+                           j > 0);
             k5::mma_commit(&acc_full[t]);
+            k5::mma_commit(&empty[s]);
           }
-          __syncwarp();
         }
       }
+      __syncwarp();
       if (leader) {
         k5::mma_commit(mma_done);
         mbar_wait(mma_done, 0);
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     // ---------------- epilogue ----------------
     const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
     const int f = quarter * 32 + lane;  // feature of the accumulator
-    float* s_scale = reinterpret_cast<float*>(smem + kOffScale) + ew * kTokens;
+    float* s_scale = reinterpret_cast<float*>(smem + kOffScale) + ew * 2 * kTokens;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * kTokens;
     uint32_t g = 0;
     Piece pc;
@@ -254,35 +256,43 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       float acc[kTokens];
 #pragma unroll
       for (int c = 0; c < kTokens; ++c) acc[c] = 0.0f;
+      // the scales of a block are in shared memory before its products are waited for: stored while the
+      // block in front is read, loaded one block earlier
       float x0 = __ldg(sx0 + pc.k0), x1 = __ldg(sx1 + pc.k0), w = __ldg(sw + pc.k0);
-      for (int b = pc.k0; b < pc.k1; ++b, ++g) {
-        const int t = g % kAccStages;
-        __syncwarp();
-        s_scale[lane] = x0 * w;
-        s_scale[lane + 32] = x1 * w;
-        __syncwarp();
+      auto next_scales = [&](int b) {  // of block b, and the loads of block b + 1
+        float* s = s_scale + (b & 1) * kTokens;
+        s[lane] = x0 * w;
+        s[lane + 32] = x1 * w;
         if (b + 1 < pc.k1) {
           x0 = __ldg(sx0 + b + 1);
           x1 = __ldg(sx1 + b + 1);
           w = __ldg(sw + b + 1);
         }
+      };
+      __syncwarp();
+      next_scales(pc.k0);
+      __syncwarp();
+      for (int b = pc.k0; b < pc.k1; ++b, ++g) {
+        const int t = g % kAccStages;
         if (!k7::warp_wait(&acc_full[t], (g / kAccStages) & 1, abort_flag)) {
           dead = true;
         } else {
           k5::tc_fence_after();
+          const float* s = s_scale + (b & 1) * kTokens;
 #pragma unroll
           for (int c0 = 0; c0 < kTokens; c0 += 16)
             if (c0 < u.rows) {
               uint32_t v[16];
               tmem_ld16(lane_addr + t * 2 * kTokens + c0, v);
+              if (c0 == 0 && b + 1 < pc.k1) next_scales(b + 1);
               tmem_wait16(v);
 #pragma unroll
               for (int c = 0; c < 16; c += 4) {
-                const float4 s = *reinterpret_cast<const float4*>(s_scale + c0 + c);
-                acc[c0 + c] = fmaf(__uint_as_float(v[c]), s.x, acc[c0 + c]);
-                acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), s.y, acc[c0 + c + 1]);
-                acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), s.z, acc[c0 + c + 2]);
-                acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), s.w, acc[c0 + c + 3]);
+                const float4 q = *reinterpret_cast<const float4*>(s + c0 + c);
+                acc[c0 + c] = fmaf(__uint_as_float(v[c]), q.x, acc[c0 + c]);
+                acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), q.y, acc[c0 + c + 1]);
+                acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), q.z, acc[c0 + c + 2]);
+                acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), q.w, acc[c0 + c + 3]);
               }
             }
         }

@@ -25,16 +25,16 @@ def type_of(t) -> int:
     return kinds[t.dtype]
 
 
-def quantize_weights(w, stream=None):
+def quantize_weights(w):
     """[E][N][K] (or [N][K]) float weights -> e4m3 bytes [E][N][K up to 16] and their scales
-    [E][N/128 up][K/128 up] (pw_scaled_quantize, blocks of 128 x 128)."""
+    [E][N/128 up][K/128 up] (pw_scaled_quantize, blocks of 128 x 128), on the current stream."""
     torch = _torch()
     lead = w.shape[:-2]
     w3 = w.reshape(-1, *w.shape[-2:]).contiguous()
     E, N, K = w3.shape
     ld = -(-K // 16) * 16
     with torch.cuda.device(w.device):
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        s = torch.cuda.current_stream().cuda_stream
         q = torch.zeros(E, N, ld, dtype=torch.uint8, device=w.device)
         scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
         for e in range(E):

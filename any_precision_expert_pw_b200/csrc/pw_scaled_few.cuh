@@ -3,16 +3,17 @@
 // weight rows x 64 tokens; gated: 128 gate rows and the 128 matching up rows) wastes nothing on rows
 // that do not exist, a lane of tensor memory is a feature, and partials, joins and outputs are
 // contiguous across lanes.  What bounds it is the weights' bytes, each read once: 5 stages of 32 KB
-// keep 160 KB an SM in flight.  64 experts of 8 rows, 5120 x 3584: 185 us, 6.4 TB/s; 4 rows x 28672 x
-// 4096 (117 MB): 24 us, of which about 5 until the first tile is there and what is left at the end.
-// From 64 rows an expert on the large-rows kernel is as fast or faster (64 x 28672 x 4096: 34.2 us
-// here, 31.1 there; 64 experts of 32 rows: 202 here, 206 there).
+// keep 160 KB an SM in flight.  64 experts of 8 rows, 5120 x 3584: 184 us, 6.4 TB/s; 4 rows x 28672 x
+// 4096 (117 MB, 112 units): 24 us, of which about 5 until the first tile is there.
+// From 64 rows an expert on the large-rows kernel is as fast or faster (64 x 28672 x 4096: 34 us here,
+// 31 there; 64 experts of 32 rows: 202 here, 206 there).
 //
 // A block's scale of a token is a column's here: the epilogue multiplies it with the weights' scale
 // once per (token, block) and reads it back from shared memory as it folds.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (two accumulators of up to 64 columns per K block, four blocks
-// in flight in tensor memory), 2 tensor memory, 4-11 epilogue: warp 4 + w has lanes (features) of
+// Warps: 0 TMA producer, 1 and 3 MMA issuers (an accumulator of up to 64 columns each, four blocks in
+// flight in tensor memory; issuing is what a block costs most when half the SMs have a unit: 76 units
+// of 4 rows, K 4096, 20.5 us with one warp for both, 19.4 with two), 2 tensor memory, 4-11 epilogue: warp 4 + w has lanes (features) of
 // quarter w % 4 of accumulator w / 4.
 #pragma once
 #include "pw_scaled.cuh"
@@ -72,7 +73,7 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
 
 // The i-th piece of a CTA: its piece of the remainder first (within one unit: pieces >= rem), then its
 // units of the whole waves, so that a join is not what the launch ends with (64 tokens through 64
-// experts 295 us, last 301).  One workspace slot a CTA.
+// experts 294.6 us, last 300.4).  One workspace slot a CTA.
 __device__ __forceinline__ bool piece_first(const Sched& s, int kb, int i, Piece& p) {
   const int cta = blockIdx.x;
   const bool extra = cta < s.pieces;  // pieces = 0 without a remainder
@@ -118,13 +119,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
     for (int b = 0; b < kAccStages; ++b) {
-      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_full[b], 2);
       mbar_init(&acc_empty[b], kEpiThreads / 32);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     mbar_fence_init();
     k7::prefetch_map(&p.xsmall);
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   const Sched sched = k7::make_sched(s_tiles[E] * p.nt, p.kb, gridDim.x, kMinPiece);
   const uint32_t smem_base = smem_u32(smem);
 
-  if (warp < 2) {
+  if (warp < 4 && warp != 2) {
     const bool leader = k7::elect_one();  // one lane issues; control flow and operands stay uniform
     uint32_t g = 0;
     Piece pc;
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         for (uint32_t x = (g > kStages ? g - kStages : 0); x < g; ++x)
           mbar_wait(&full[x % kStages], (x / kStages) & 1);
     } else {
-      // ---------------- MMA issuer ----------------
+      // ---------------- MMA issuers: warp 1 accumulator 0, warp 3 accumulator 1 ----------------
+      const int h = warp >> 1;
       griddep_wait();  // nothing to multiply before; the bounded waits below start after it
-      const uint64_t wd0 = k7::sw128_desc(smem_base);
+      const uint64_t xd0 = k7::sw128_desc(smem_base + kWBytes);
       for (int i = 0; ok && piece_first(sched, p.kb, i, pc); ++i) {
         const Unit u = k7::find_unit<kTokens>(p, s_tiles, s_first, pc.unit);
         const uint32_t id = instr((u.rows + kBox - 1) / kBox * kBox);
@@ -216,15 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                                     abort_flag)))
             break;
           k5::tc_fence_after();
-          const uint64_t wd = wd0 + static_cast<uint64_t>(s) * (kStageBytes / 16);
-          const uint32_t d = tmem_base + t * 2 * kTokens;
+          const uint64_t xd = xd0 + static_cast<uint64_t>(s) * (kStageBytes / 16);
+          const uint64_t wd = xd - (2 - h) * (kWBytes / 2 / 16);
+          const uint32_t d = tmem_base + (2 * t + h) * kTokens;
           if (leader) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)  // 32 bytes of K each
-                k7::mma_f8(d + h * kTokens, wd + h * (kWBytes / 2 / 16) + 2 * j, wd + kWBytes / 16 + 2 * j, id,
-                           j > 0);
+            for (int j = 0; j < 4; ++j)  // 32 bytes of K each
+              k7::mma_f8(d, wd + 2 * j, xd + 2 * j, id, j > 0);
             k5::mma_commit(&acc_full[t]);
             k5::mma_commit(&empty[s]);
           }

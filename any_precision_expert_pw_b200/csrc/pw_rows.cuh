@@ -141,7 +141,8 @@ __device__ __forceinline__ int checked_row(const int32_t* pos, long long slot, i
 // walks its part again and takes places in order.  Equal ids inside a step of 32 are ranked with one
 // warp match.  With more than one CTA a first launch leaves each CTA's counts in the workspace and
 // every CTA sums the ones before its own (at most one CTA per SM, so at most SMs x E values from
-// L2).  Latency bound: two walks over the ids and three block-wide steps.
+// L2).  Latency bound: two walks over the ids and three block-wide steps (131072 slots of 64 experts:
+// 14 us in two launches; 160 slots of 512 experts: 5 us).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 4;  // steps whose ids are loaded before the first is used
@@ -335,7 +336,9 @@ __global__ void zero_words_kernel(int32_t* p, int n) {
 }
 
 // ---- dispatch ----
-// One warp: token t, 32 x U units of 16 bytes (VEC) or of one element (2 or 4 bytes).
+// One warp: token t, 32 x U units of 16 bytes or of one element (2 or 4 bytes), read once and written
+// to the token's k rows.  Bound by the bytes written (16384 tokens x 8 x 3584 bf16, 1.03 GB: 162 us,
+// 6.3 TB/s).
 template <typename UNIT, int U>
 __global__ void __launch_bounds__(256) dispatch_kernel(const UNIT* x, int T, int k, int units,
                                                        size_t ld_x, const int32_t* pos, UNIT* xs,
@@ -364,8 +367,9 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const UNIT* x, int T, int
 }
 
 // ---- combine, and the gradient of dispatch (gate = NULL: weights of one) ----
-// One warp: token t, 32 x U vectors of V elements; four sorted rows in flight; fp32 sums in slot
-// order.
+// One warp: token t, 32 x U vectors of V elements; four sorted rows in flight, as they lie in memory;
+// fp32 sums in slot order.  Bound by the bytes read (8192 tokens x 4 x 2048 fp32, 332 MB: 53 us; 4096 x
+// 8 x 3584 bf16, 264 MB: 41 us; with the rows converted as they arrive the latter took 66, registers).
 template <int TI, int TO, int V, int U>
 __global__ void __launch_bounds__(256) combine_rows_kernel(const void* o, int T, int k, int H,
                                                            size_t ld_o, const int32_t* pos,
@@ -425,6 +429,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const void* o, int T,
 // ---- gradient of combine ----
 // One CTA per token: dy[t] is read once; per column vector the k rows of o are read, their products
 // with dy summed per slot (fp32, then a fixed tree over the block), and g dy written to the k rows.
+// Bound by the bytes (4096 x 8 x 3584 bf16, 499 MB: 77 us, 6.5 TB/s; 512 threads 97, 128 84).
 constexpr int kGradThreads = 256;
 
 template <int TY, int V, int KM>
@@ -539,7 +544,8 @@ __device__ __forceinline__ uint32_t e4m3_word(float a, float b, float c, float d
 // One half-warp per (row, 128-column block), 8 columns a lane, U rows in flight; a CTA's sixteen
 // half-warps take up to 16 blocks of a row (blockIdx.y: the next 16), and rp rows side by side where a
 // row has fewer.  pos == NULL: to row t of q; else to the rows of the token's k slots (quantise and
-// dispatch in one pass).  Bound by the bytes.
+// dispatch in one pass).  4096 x 3584 bf16: 11.8 us (44 MB; 16.4 with fp32 values throughout), to 8 rows
+// each 30 us (150 MB).
 template <int TY, bool VEC, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, long long rows, int cols,
                                                             size_t ld_x, int k, const int32_t* pos,

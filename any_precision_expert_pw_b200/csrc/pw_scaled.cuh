@@ -207,8 +207,10 @@ __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volati
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
 #pragma unroll 1
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 8; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
   return wait_slow(bar, parity, abort_flag);
 }
 
@@ -225,6 +227,13 @@ __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b
   const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
   if (__all_sync(0xffffffffu, ra && rb)) return true;
   return __all_sync(0xffffffffu, wait_bar(a, pa, abort_flag) && wait_bar(b, pb, abort_flag));
+}
+
+// Test hook (pw_test_hold_down_items): an issuing warp waits for products that never come, so that
+// every bounded wait of the block runs out.  True in normal use.
+__device__ __forceinline__ bool not_held(uint64_t* never, volatile int* abort_flag) {
+  if (*static_cast<volatile int*>(&g_test_hold) == 0) return true;
+  return warp_wait(never, 0, abort_flag);
 }
 
 // ---- tcgen05 / TMA ----
@@ -525,11 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
           mbar_wait(&full[x % kStages], (x / kStages) & 1);
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
+      bool ok = not_held(mma_done, abort_flag);
       griddep_wait();  // nothing to multiply before; the bounded waits below start after it
       const uint64_t ad0 = sw128_desc(smem_base);
       uint32_t g = 0;
       Piece pc;
-      bool ok = true;
       for (int i = 0; ok && get_piece(sched, p.kb, i, pc); ++i) {
         for (int b = pc.k0; b < pc.k1; ++b, ++g) {
           const int s = g % kStages, t = g & 1;

@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     } else {
       // ---------------- MMA issuers: warp 1 accumulator 0, warp 3 accumulator 1 ----------------
       const int h = warp >> 1;
+      ok = k7::not_held(mma_done, abort_flag);
       griddep_wait();  // nothing to multiply before; the bounded waits below start after it
       const uint64_t xd0 = k7::sw128_desc(smem_base + kWBytes);
       for (int i = 0; ok && piece_first(sched, p.kb, i, pc); ++i) {

@@ -369,6 +369,8 @@ pw_status pw_set_tc_min_tokens(int tokens_per_expert);
  * pw_test_hold_down_items: every down item of the fused FFN launch on the current device waits
  *   for `extra` more gate_up completions than exist, so its bounded wait runs out and the
  *   forward ends with PW_ERR_TIMEOUT (the failure path of a gate_up tile that never finishes).
+ *   A positive value also makes the scaled products (pw_scaled_gemm, pw_moe_scaled_forward) wait
+ *   for operands that never come: they end with PW_ERR_TIMEOUT and write zeros.
  *   0 (default) restores normal behaviour.  Synchronous, like pw_set_wait_limit_ns.
  * ------------------------------------------------------------------------------------- */
 pw_status pw_set_ffn_grid(int ctas);

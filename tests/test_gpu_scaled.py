@@ -406,3 +406,40 @@ def test_products_beyond_32_bits(libpw):
     xv = S.values(*S.quantize(x[pick].double().cpu().numpy(), 1), 1)
     ref, mag = xv @ v[0].T, np.abs(xv) @ np.abs(v[0]).T
     assert (np.abs(y[pick][:, :N].double().cpu().numpy() - ref) <= (sum_bound(K // 128) + U) * mag).all()
+
+
+@pytest.mark.parametrize("M", [5, 300])                    # both kernels
+def test_wait_that_never_completes_times_out(libpw, M):
+    """The issuers wait for operands that never come: the call returns, the status reads PW_ERR_TIMEOUT
+    once, the tiles are zeros, and the next call is right."""
+    import torch
+    N, K = 600, 4096
+    q, s, v = weights(1, N, K, 25)
+    w, ldw = padded_codes(q)
+    ws = gpu(s)
+    x = torch.randn(M, K, device="cuda")
+    xq, xs = torch.empty(M, K, dtype=torch.uint8, device="cuda"), torch.empty(M, K // 128, device="cuda")
+    B.check(B.pw_scaled_quantize(x.data_ptr(), B.PW_TYPE_F32, M, K, K, 1, xq.data_ptr(), K, xs.data_ptr()))
+    n = B.pw_scaled_gemm_workspace_bytes(M, N, K, 1)
+    tmp = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def run():
+        y = torch.full((M, N), -7.0, device="cuda")
+        B.check(B.pw_scaled_gemm(xq.data_ptr(), xs.data_ptr(), M, K, K, w.data_ptr(), ws.data_ptr(), 1, N, ldw, 0,
+                                 y.data_ptr(), B.PW_TYPE_F32, N, tmp.data_ptr(), n))
+        return y, B.pw_get_status()
+
+    try:
+        B.check(B.pw_set_wait_limit_ns(5_000_000))          # 5 ms
+        B.check(B.pw_test_hold_down_items(1))
+        y, st = run()
+        assert st == B.PW_ERR_TIMEOUT and B.pw_get_status() == B.PW_OK
+        assert bool((y == 0).all())
+    finally:
+        B.check(B.pw_test_hold_down_items(0))
+        B.check(B.pw_set_wait_limit_ns(0))
+    y, st = run()
+    assert st == B.PW_OK
+    xv = S.values(*S.quantize(x.double().cpu().numpy(), 1), 1)
+    ref, mag = xv @ v[0].T, np.abs(xv) @ np.abs(v[0]).T
+    assert (np.abs(y.double().cpu().numpy() - ref) <= (sum_bound(K // 128) + U) * mag).all()

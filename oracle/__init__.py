@@ -35,6 +35,10 @@ integer-valued LUTs that expose the decoded indices, all-resident = identity, +i
 first-choice rule, critical set covering every chosen expert = identity), and invariants
 (exactly k distinct experts per token, top-1 never substituted, rank-0 never remapped).
 
+rows.py and scaled.py (token rows sorted by expert and back with their gradients; e4m3 values, block
+scales and products on them) restate definitions of this library, not of the pages; they are pinned by
+hand cases, differences and an independent e4m3 cast.
+
 Parity unpinned: affinity.py (AffinityBinning).  The pages name its parts but give no formula,
 so what it computes is this project's reading (stated in its docstring); it is pinned against
 hand cases, a brute-force bin definition and the batch remap it reduces to, not against the

@@ -133,9 +133,9 @@ struct ScaledCall {
 };
 
 // Rows per expert (on average over the experts that can have one) up to which the few-rows kernel is
-// used: with 32 it is ahead (64 experts x 32 rows, 5120 x 3584: 202 us against 206; one matrix, 32 rows:
-// 18 against 34), with 64 behind (219 against 216; 64 x 28672 x 4096: 34 against 31), and ragged groups
-// of 50 rows on average, many above 64, take 93 against 85.
+// used: with 32 it is ahead (64 experts x 32 rows, 5120 x 3584: 194 us against 206; one matrix, 32 rows:
+// 16.7 against 20.6), with 64 even or behind (212 against 214; 64 x 28672 x 4096: 36 against 31), and
+// ragged groups of 50 rows on average, many above 64, take 96 against 80.
 constexpr int kFewRows = 32;
 
 int part_rows(int M) { return static_cast<int>(align_up(std::min(M, pw::k7::kTileM), 32)); }

@@ -5,8 +5,8 @@
 // contiguous across lanes.  What bounds it is the weights' bytes, each read once: 5 stages of 32 KB
 // keep 160 KB an SM in flight.  64 experts of 8 rows, 5120 x 3584: 184 us, 6.4 TB/s; 4 rows x 28672 x
 // 4096 (117 MB, 112 units): 24 us, of which about 5 until the first tile is there.
-// From 64 rows an expert on the large-rows kernel is as fast or faster (64 x 28672 x 4096: 34 us here,
-// 31 there; 64 experts of 32 rows: 202 here, 206 there).
+// From 64 rows an expert on the large-rows kernel is as fast or faster (64 x 28672 x 4096: 36 us here,
+// 31 there; 64 experts of 32 rows: 194 here, 206 there).
 //
 // A block's scale of a token is a column's here: the epilogue multiplies it with the weights' scale
 // once per (token, block) and reads it back from shared memory as it folds.

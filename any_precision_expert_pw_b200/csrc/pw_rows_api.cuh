@@ -140,7 +140,7 @@ constexpr int kFewRows = 32;
 
 int part_rows(int M) { return static_cast<int>(align_up(std::min(M, pw::k7::kTileM), 32)); }
 size_t part_bytes(int M) {
-  return sizeof(float) * 2 * kScaledMaxGrid * pw::k7::kTileN * static_cast<size_t>(part_rows(M));
+  return sizeof(float) * kScaledMaxGrid * pw::k7::kTileN * static_cast<size_t>(part_rows(M));
 }
 
 pw_status launch_scaled(const ScaledCall& c, int sms, cudaStream_t st) {

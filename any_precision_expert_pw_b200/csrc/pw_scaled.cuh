@@ -86,7 +86,7 @@ struct alignas(64) Params {
   uint8_t* hq;  // gated: e4m3 [M][I], fp32 scales [M][I / 128]
   float* hs;
   int I;
-  float* part;       // [2 per CTA][256][rcap]
+  float* part;       // [CTA][256][rcap]
   int rcap;
   int32_t* counter;  // [CTAs], zero at launch
 };
@@ -116,10 +116,10 @@ __device__ __forceinline__ int piece_of(const Sched& s, int x) {  // the piece t
 }
 struct Piece {
   int unit, k0, k1;
-  int first, count, slot;  // pieces of the unit, and this one's workspace slot
+  int first, count, slot;  // the unit's pieces are those of CTAs first ..; one workspace slot a CTA
 };
-// The i-th piece of a CTA.  A piece of the remainder is at most one unit long (pieces >= rem), so
-// it touches at most two units.
+// The i-th piece of a CTA: its units of the whole waves, then its piece of the remainder (within one
+// unit: pieces is a multiple of rem).
 __device__ __forceinline__ bool get_piece(const Sched& s, int kb, int i, Piece& p) {
   const int cta = blockIdx.x;
   p.first = 0;
@@ -131,22 +131,14 @@ __device__ __forceinline__ bool get_piece(const Sched& s, int kb, int i, Piece& 
     p.k1 = kb;
     return true;
   }
-  if (s.rem == 0 || cta >= s.pieces) return false;
-  int a = piece_begin(s, cta);
-  const int b = piece_begin(s, cta + 1);
-  const int j0 = a / kb;
-  if (i > s.waves) {
-    if (i > s.waves + 1) return false;
-    a = (j0 + 1) * kb;
-  }
-  if (a >= b) return false;
-  const int j = a / kb;
+  if (i > s.waves || cta >= s.pieces) return false;  // pieces = 0 without a remainder
+  const int a = piece_begin(s, cta), b = piece_begin(s, cta + 1), j = a / kb;
   p.unit = s.waves * static_cast<int>(gridDim.x) + j;
   p.k0 = a - j * kb;
-  p.k1 = min(kb, p.k0 + b - a);
+  p.k1 = p.k0 + b - a;
   p.first = piece_of(s, j * kb);
   p.count = piece_of(s, (j + 1) * kb - 1) - p.first + 1;
-  p.slot = 2 * cta + (i > s.waves ? 1 : 0);
+  p.slot = cta;
   return true;
 }
 
@@ -652,10 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_kernel(const __grid_consta
         if (!last_piece(p.counter + (done.unit - sched.waves * static_cast<int>(gridDim.x)), done.count, s_last))
           continue;
         if (live) {
-          const int j = done.unit - sched.waves * static_cast<int>(gridDim.x);
           auto piece_at = [&](int q) {
-            const int slot = 2 * q + (piece_begin(sched, q) / p.kb == j ? 0 : 1);
-            return p.part + slot * slot_floats + static_cast<size_t>(half * 128) * p.rcap + r;
+            return p.part + q * slot_floats + static_cast<size_t>(half * 128) * p.rcap + r;
           };
           if (done.count == 2) {  // the other piece onto this one, in registers: the order is no matter
             const float* d = piece_at(2 * done.first + 1 - static_cast<int>(blockIdx.x));

@@ -13,8 +13,8 @@
 //
 // Warps: 0 TMA producer, 1 and 3 MMA issuers (an accumulator of up to 64 columns each, four blocks in
 // flight in tensor memory; issuing is what a block costs most when half the SMs have a unit: 76 units
-// of 4 rows, K 4096, 20.5 us with one warp for both, 19.4 with two), 2 tensor memory, 4-11 epilogue: warp 4 + w has lanes (features) of
-// quarter w % 4 of accumulator w / 4.
+// of 4 rows, K 4096, 20.5 us with one warp for both, 19.4 with two), 2 tensor memory, 4-11 epilogue:
+// warp 4 + w has lanes (features) of quarter w % 4 of accumulator w / 4.
 #pragma once
 #include "pw_scaled.cuh"
 

@@ -140,12 +140,14 @@ __device__ __forceinline__ int checked_row(const int32_t* pos, long long slot, i
 // sorting network: count per (warp, expert), prefix over warps, CTAs and experts, then each warp
 // walks its part again and takes places in order.  Equal ids inside a step of 32 are ranked with one
 // warp match.  With more than one CTA a first launch leaves each CTA's counts in the workspace and
-// every CTA sums the ones before its own (at most one CTA per SM, so at most SMs x E values from
-// L2).  Latency bound: two walks over the ids and three block-wide steps (131072 slots of 64 experts:
-// 14 us in two launches; 160 slots of 512 experts: 5 us).
+// every CTA sums the ones before its own (one CTA per SM, 257 for the largest batch, so at most 257 x
+// E values from L2).  A warp's counts, and its first places within the CTA's run, are 16 bits: a run
+// has at most kSortMaxRun slots, whatever its ids.  Latency bound: two walks over the ids and three
+// block-wide steps (131072 slots of 64 experts: 14 us in two launches; 160 slots of 512 experts: 5 us).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortAhead = 4;  // steps whose ids are loaded before the first is used
+constexpr int kSortMaxRun = 65535;  // slots of a CTA's run
+constexpr int kSortAhead = 4;       // steps whose ids are loaded before the first is used
 
 // Warps that share a run of n slots: whole steps of 32 each, no more warps than steps (fewer rows of
 // the count table to clear and to sum).

@@ -25,12 +25,14 @@ inline bool vec_ok(const void* p, int size, int H, long long ld) {
 }
 
 // A sort of n slots uses one CTA up to kSortOne (both measured: there a second launch costs more
-// than the longer walk), then one per kSortRun slots, at most one per SM.
+// than the longer walk), then one per kSortRun slots, at most one per SM; more than that only where a
+// CTA's run would pass what its 16-bit places hold (pw::kSortMaxRun: from 9.7 million slots on).
 constexpr int kSortOne = 8192;
 constexpr int kSortRun = 1024;
+static_assert(kSortOne <= pw::kSortMaxRun && kSortRun <= pw::kSortMaxRun, "16-bit places");
 int sort_ctas(int n, int sms) {
   if (n <= kSortOne) return 1;
-  return std::min(sms, (n + kSortRun - 1) / kSortRun);
+  return std::max(std::min(sms, (n + kSortRun - 1) / kSortRun), (n + pw::kSortMaxRun - 1) / pw::kSortMaxRun);
 }
 
 struct ScaledDevice {
@@ -194,8 +196,6 @@ pw_status launch_sort(const int32_t* idx, int T, int k, int E, int32_t* pos, int
                       cudaStream_t st) {
   const int n = T * k, ctas = sort_ctas(n, std::min(sms, kScaledMaxGrid));
   const dim3 block(pw::kSortThreads);
-  // a warp counts its part in 16 bits (148 CTAs: 3543 slots at most)
-  if (n / ctas / pw::kSortWarps >= 65535) return PW_ERR_UNSUPPORTED;
   if (ctas > 1 &&
       launch_dependent(pw::sort_count_kernel, dim3(ctas), block,
                        2 * pw::kSortWarps * static_cast<size_t>(E), st, idx, n, E, part) != PW_OK)

@@ -88,6 +88,41 @@ def test_sort_one_expert_and_repeated_ids(libpw):
     assert off.cpu().numpy().tolist() == [0, 0, 0, 0, 200, 200]
 
 
+@pytest.mark.parametrize("T,k,E,kind", [(1 << 24, 1, 1, "one"), (1 << 24, 1, 3, "dominant"),
+                                        (1 << 20, 16, 1024, "blocks"), (650_001, 15, 2, "dominant")])
+def test_sort_largest_batches(libpw, T, k, E, kind):
+    """The largest batches, most of a run's slots on one expert: every row once, in slot order."""
+    import torch
+    n = T * k
+    if kind == "one":
+        flat = torch.zeros(n, dtype=torch.int32, device="cuda")
+    elif kind == "dominant":                     # 3 of 100 slots elsewhere or empty
+        g = torch.Generator(device="cuda")
+        g.manual_seed(n)
+        flat = torch.full((n,), E - 1, dtype=torch.int32, device="cuda")
+        other = torch.rand(n, generator=g, device="cuda") < 0.03
+        flat[other] = torch.randint(-1, E, (int(other.sum()),), generator=g, device="cuda", dtype=torch.int32)
+    else:                                        # long runs of one id, each longer than a CTA's run
+        flat = (torch.arange(n, device="cuda") // 200_000 * 37 % E).int()
+    pos = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    src = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    off = torch.full((E + 1,), -7, dtype=torch.int32, device="cuda")
+    size = B.pw_expert_sort_workspace_bytes(T, k, E)
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    B.check(B.pw_expert_sort(flat.data_ptr(), T, k, E, pos.data_ptr(), src.data_ptr(), off.data_ptr(),
+                             ws.data_ptr(), size))
+    assert B.pw_get_status() == B.PW_OK and bool((ws[size:] == 0xA5).all())
+    key = torch.where(flat < 0, E, flat)
+    order = torch.sort(key, stable=True).indices
+    live = int((flat >= 0).sum())
+    assert bool((src[:live] == order[:live]).all()) and bool((src[live:] == -7).all())
+    want = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    want[order[:live]] = torch.arange(live, dtype=torch.int32, device="cuda")
+    assert bool((pos == want).all())
+    count = torch.bincount(key.long(), minlength=E + 1)[:E]
+    assert off.tolist() == [0] + torch.cumsum(count, 0).tolist()
+
+
 @pytest.mark.parametrize("T", [9, 3000])
 def test_sort_records_bad_ids(libpw, T):
     idx = routing(T, 6, 3, 2)

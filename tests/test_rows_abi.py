@@ -29,6 +29,15 @@ def test_sort_refusals(libpw):
           dict(idx=P + 2), dict(pos=P + 1)])
 
 
+@pytest.mark.parametrize("T,k", [(1 << 24, 1), (1 << 20, 16), (600_000, 16), (9_800_000, 1), (70_001, 2)])
+def test_sort_runs_fit_their_places(libpw, T, k):
+    """Places within the run of a sort's CTA are 16 bits: the count table (one int32 per CTA and
+    expert) has enough CTAs that no run is longer than 65535 slots, on any number of SMs."""
+    E = 64                                       # 4 E = 256: the table's size has no padding
+    ctas = B.pw_expert_sort_workspace_bytes(T, k, E) // (4 * E)
+    assert -(-T * k // ctas) <= 65535
+
+
 def test_row_movement_refusals(libpw):
     good = dict(x=P, type_=BF16, T=8, k=2, H=64, x_stride=64, pos=P, xs=P, xs_stride=64)
     _bad(B.pw_expert_dispatch, good,

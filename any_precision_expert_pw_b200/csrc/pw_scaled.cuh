@@ -374,7 +374,9 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, void* y, size_t row0,
 }
 
 // Row tiles (of TM rows) before each expert, from the offsets: tiles[E + 1], first[E + 1] in shared
-// memory; offsets that decrease or leave [0, M] give no rows and are recorded.  Whole block.
+// memory.  Offsets that decrease or leave [0, M] are recorded; a group that would start before an
+// earlier offset gets no rows, so groups are disjoint (no row has two writers) and there are at most
+// M / TM + E tiles whatever the offsets hold.  Whole block.
 template <int TM>
 __device__ __forceinline__ void row_tiles(const Params& p, int* tiles, int* first) {
   const int E = p.E;
@@ -387,14 +389,19 @@ __device__ __forceinline__ void row_tiles(const Params& p, int* tiles, int* firs
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int carry = 0;
+    int top = -1;  // from the first 32 experts on whose offsets decrease: the largest offset before
     for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      int v = 0;
-      if (e < E) {
-        const int rows = first[e + 1] - first[e];
-        if (rows < 0) set_status(PW_ERR_BOUNDS);
-        v = rows > 0 ? (rows + TM - 1) / TM : 0;
+      const int e = e0 + lane, a = e < E ? first[e] : 0;
+      int rows = e < E ? first[e + 1] - a : 0;
+      if (rows < 0) set_status(PW_ERR_BOUNDS);
+      if (__any_sync(0xffffffffu, rows < 0) || top >= 0) {
+        int m = max(a, top);  // largest offset up to this one
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) m = max(m, __shfl_up_sync(0xffffffffu, m, d));
+        if (a < m) rows = 0;
+        top = __shfl_sync(0xffffffffu, m, 31);
       }
+      int v = rows > 0 ? (rows + TM - 1) / TM : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, v, d);

@@ -517,8 +517,9 @@ pw_status pw_scaled_quantize(const void* x, int type, int rows, int cols, long l
  *   16, K of each row used), x_scale [M][ceil(K / 128)],
  *   w_scale [E][ceil(N / 128)][ceil(K / 128)], offsets [E + 1] int32 on the device as
  *   pw_expert_sort writes them (NULL with E = 1: all M rows), y [M][y_stride] of y_type.
- *   An expert may have no rows.  Offsets that decrease or leave [0, M] record PW_ERR_BOUNDS,
- *   and the rows they do not give are left as they were.
+ *   An expert may have no rows.  Offsets that decrease or leave [0, M] record PW_ERR_BOUNDS: they
+ *   are taken into [0, M], a group that starts before an earlier offset has no rows, and the rows
+ *   that no group has are left as they were.
  *   1 <= M <= PW_MAX_ROWS; 1 <= N, K, strides <= PW_MAX_COLS.  A square block transposes
  *   with its scale, so the gradient d_x = d_y W is this call on W^T (K and N exchanged).
  *   workspace: >= pw_scaled_gemm_workspace_bytes(M, N, K, E) bytes (0 on bad sizes), 256-byte

@@ -199,6 +199,57 @@ def test_bad_offsets_are_recorded(libpw, off):
     assert ((got == 0) | (got == -77.0)).all()
 
 
+def groups_of(off, M):
+    """The rows that offsets give: taken into [0, M], no group starts before an earlier offset."""
+    o = np.clip(off, 0, M)
+    return [(o[e], o[e + 1]) if o[e] >= max(o[:e + 1]) else (o[e], o[e]) for e in range(len(o) - 1)]
+
+
+@pytest.mark.parametrize("scale", [1, 100])                # 100: the large-rows kernel
+@pytest.mark.parametrize("off", [[0, 5, 3, 8], [0, 4, 20, 8], [-3, 2, 4, 8], [8, 0, 0, 0], [2, 6, 1, 8, 3, 8],
+                                 [0, 8, 0, 8, 0, 8], [3, 1, 5, 6, 2, 7]])
+def test_bad_offsets_keep_groups_apart(libpw, off, scale):
+    """The valid groups are right, every other row is left as it was: no row has two writers."""
+    off, M, N, K, E = np.array(off) * scale, 8 * scale, 300, 200, len(off) - 1
+    check_groups(off, M, N, K, E)
+
+
+def test_bad_offsets_of_many_experts(libpw):
+    """A decrease in the middle of 200 experts, and one after it: looked at 32 experts at a time."""
+    rows = np.random.default_rng(26).integers(0, 4, 200)
+    off = np.concatenate([[0], np.cumsum(rows)])
+    M = int(off[-1])
+    off[77] -= 40
+    off[130] = M
+    check_groups(off, M, 130, 128, 200)
+
+
+def check_groups(off, M, N, K, E):
+    import torch
+    rng = np.random.default_rng([M, E])
+    q, s, v = weights(E, N, K, 27)
+    w, ldw = padded_codes(q)
+    x = gpu(rng.normal(size=(M, K)).astype(np.float32))
+    ld = -(-K // 16) * 16
+    xq, xs = torch.full((M, ld), 127, dtype=torch.uint8, device="cuda"), torch.empty(M, -(-K // 128), device="cuda")
+    B.check(B.pw_scaled_quantize(x.data_ptr(), B.PW_TYPE_F32, M, K, K, 1, xq.data_ptr(), ld, xs.data_ptr()))
+    y, ws, o = Strided(M, N, "f32", 4, 64), gpu(s), gpu(np.asarray(off, np.int32))
+    n = B.pw_scaled_gemm_workspace_bytes(M, N, K, E)
+    tmp = torch.empty(n, dtype=torch.uint8, device="cuda")
+    B.check(B.pw_scaled_gemm(xq.data_ptr(), xs.data_ptr(), M, K, ld, w.data_ptr(), ws.data_ptr(), E, N, ldw,
+                             o.data_ptr(), y.ptr, B.PW_TYPE_F32, y.ld, tmp.data_ptr(), n))
+    assert B.pw_get_status() == B.PW_ERR_BOUNDS
+    xv = S.values(*S.quantize(x.double().cpu().numpy(), 1), 1)
+    got, left = y.np(), np.ones(M, bool)
+    for e, (a, b) in enumerate(groups_of(off, M)):
+        if a < b:
+            assert left[a:b].all()
+            left[a:b] = False
+            ref, mag = xv[a:b] @ v[e].T, np.abs(xv[a:b]) @ np.abs(v[e]).T
+            assert (np.abs(got[a:b] - ref) <= (sum_bound(-(-K // 128)) + U) * mag).all()
+    assert (got[left] == -77.0).all() and y.outside_untouched()
+
+
 def _layer(H, I, E, seed):
     q1, s1, v1 = weights(E, 2 * I, H, seed)
     q2, s2, v2 = weights(E, H, I, seed + 1)

@@ -326,9 +326,12 @@ __device__ __forceinline__ void fold32(float* acc, const uint32_t (&r)[32], floa
   }
 }
 
-// SiLU(g) * u.  The hardware exponential and reciprocal (errors of a few 2^-22) are far below the
-// 2^-4 step of the e4m3 value that h becomes.
-__device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// SiLU(g) * u.  With t = e^-|g| the sigmoid is 1 / (1 + t), or t / (1 + t) for a negative g: t is at most
+// one, so no g overflows it and the denominator is in [1, 2], where the fast division holds (2 units).
+__device__ __forceinline__ float gated(float g, float u) {
+  const float t = __expf(-fabsf(g));
+  return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;
+}
 
 // A warp's 32 rows x 128 columns (a thread holds one row's) to y, through a staging buffer of 32 rows
 // x 64 bytes (rows 80 bytes apart: conflict free both ways), so that a store instruction writes

@@ -512,7 +512,9 @@ pw_status pw_scaled_quantize(const void* x, int type, int rows, int cols, long l
  * pw_scaled_gemm: y = x W^T with both operands in e4m3, one matrix or one per expert:
  *   y[r][n] = sum over blocks b of x_scale[r][b] * w_scale[e][n / 128][b] *
  *             sum over the 128 columns c of b of x_q[r][c] * w_q[e][n][c],
- *   e the expert with offsets[e] <= r < offsets[e + 1].  Scales are any fp32 numbers.
+ *   e the expert with offsets[e] <= r < offsets[e + 1].  Scales are any fp32 numbers whose product
+ *   x_scale * w_scale, formed first, is in fp32's range: from 2^128 on it is infinite (and NaN with a
+ *   sum of 0), below 2^-126 its rounding adds up to 2^-125 a block to the error of y.
  *   x_q [M][x_stride], w_q [E][N][w_stride] e4m3 bytes (16-byte aligned, strides multiples of
  *   16, K of each row used), x_scale [M][ceil(K / 128)],
  *   w_scale [E][ceil(N / 128)][ceil(K / 128)], offsets [E + 1] int32 on the device as

@@ -199,6 +199,36 @@ def test_bad_offsets_are_recorded(libpw, off):
     assert ((got == 0) | (got == -77.0)).all()
 
 
+@pytest.mark.parametrize("M", [5, 70])                     # both kernels
+def test_product_of_extreme_scales(libpw, M):
+    """The product of two scales is rounded to fp32 first.  In the normal range that costs what
+    sum_bound grants; below 2^-126 its absolute error is half of 2^-149, and |P| <= 128 * 448^2 < 2^25, so
+    a block adds less than 2^-125."""
+    import torch
+    N, K = 140, 256
+    rng = np.random.default_rng([28, M])
+    q, _, _ = weights(1, N, K, 29)
+    xq = S.round_e4m3(np.clip(rng.normal(size=(M, K)) * 120, -448, 448))
+    e = np.array([[-126, -126], [120, -100], [-126, 100], [90, 119], [-60, 0]])
+    xs = 2.0 ** e[np.arange(M) % 5]
+    ws = (np.array([[[2.0 ** -20, 2.0 ** -12], [2.0 ** -13, 1.0]]]) * 1.1875).astype(np.float32)
+    w, ldw = padded_codes(q)
+    d = [gpu(xq), gpu(xs.astype(np.float32)), gpu(ws)]
+    y, n = torch.empty(M, N, device="cuda"), B.pw_scaled_gemm_workspace_bytes(M, N, K, 1)
+    tmp = torch.empty(n, dtype=torch.uint8, device="cuda")
+    B.check(B.pw_scaled_gemm(d[0].data_ptr(), d[1].data_ptr(), M, K, K, w.data_ptr(), d[2].data_ptr(), 1, N, ldw, 0,
+                             y.data_ptr(), B.PW_TYPE_F32, N, tmp.data_ptr(), n))
+    assert B.pw_get_status() == B.PW_OK
+    xv, v = S.values(xq, xs, 1), S.values(q[0], ws[0], 128)
+    with np.errstate(over="ignore"):
+        ref, mag = xv @ v.T, np.abs(xv) @ np.abs(v).T
+    got = y.double().cpu().numpy()
+    fits = np.broadcast_to(mag < 2.0 ** 127, got.shape)
+    assert (np.abs(got - ref)[fits] <= (sum_bound(2) * mag + 2 * 2.0 ** -125)[fits]).all()
+    assert fits[[0, 1, 4]].all() and np.isfinite(got[fits]).all()
+    assert (np.abs(ref[0]) < 2.0 ** -100).any() and (got[0] != 0).all()
+
+
 def groups_of(off, M):
     """The rows that offsets give: taken into [0, M], no group starts before an earlier offset."""
     o = np.clip(off, 0, M)

@@ -225,7 +225,7 @@ def test_product_of_extreme_scales(libpw, M):
     got = y.double().cpu().numpy()
     fits = np.broadcast_to(mag < 2.0 ** 127, got.shape)
     assert (np.abs(got - ref)[fits] <= (sum_bound(2) * mag + 2 * 2.0 ** -125)[fits]).all()
-    assert fits[[0, 1, 4]].all() and np.isfinite(got[fits]).all()
+    assert fits[[0, 2, 4]].all() and fits[1].any() and np.isfinite(got[fits]).all()
     assert (np.abs(ref[0]) < 2.0 ** -100).any() and (got[0] != 0).all()
 
 

@@ -326,8 +326,12 @@ __device__ __forceinline__ void fold32(float* acc, const uint32_t (&r)[32], floa
   }
 }
 
-// SiLU(g) * u.  With t = e^-|g| the sigmoid is 1 / (1 + t), or t / (1 + t) for a negative g: t is at most
-// one, so no g overflows it and the denominator is in [1, 2], where the fast division holds (2 units).
+// SiLU(g) * u.  With t = e^-|g| the sigmoid is 1 / (1 + t), or t / (1 + t) for a negative g: t never
+// overflows and the denominator is in [1, 2], where the fast division holds (2 units in the last place;
+// e^-g itself would pass 2^126 at g = -87.4, from where that division returns 0).  The fast exponential
+// is off by up to 2 + 1.2 |g| units, so for negative g the result is too, by 2^-18 of its value at -20
+// and 2^-16 at -87: far below the half step, 2^-4, of the e4m3 value it becomes next.  (With expf
+// the prompt layer of 4096 tokens takes 2 % longer.)
 __device__ __forceinline__ float gated(float g, float u) {
   const float t = __expf(-fabsf(g));
   return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;

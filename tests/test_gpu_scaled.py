@@ -318,6 +318,44 @@ def test_layer(libpw, T, k, E, H, I, xt, yt):
     assert float(np.median(tol)) < 0.05 * float(np.sqrt((ref ** 2).mean()))
 
 
+@pytest.mark.parametrize("n", [2, 40])                     # tokens an expert: both kernels
+def test_layer_of_very_negative_gates(libpw, n):
+    """SiLU(g) u where e^-g passes 2^126 and 2^128 and u makes up for it.  x has one value, so g and u are
+    known (one rounding, of g); h is off by (8 + 1.2 |g|) units (moe_bound), at most 2^-16 of its value,
+    and where e^g is subnormal by half of 2^-149 in e^g >= 2^-133, another 2^-17: below 2^-15 in all.  It
+    becomes its e4m3 value or, within that of a border, the next one."""
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    gs = [-92.0, -89.5, -88.6, -88.0, -87.5, -86.0, -60.0, -20.0, -1.0, 0.0, 1.0, 30.0, 88.0]
+    E, H, I, T = len(gs), 128, 128, len(gs) * n
+    rng = np.random.default_rng(30)
+    q1, q2 = np.zeros((E, 2 * I, H), np.uint8), S.round_e4m3(rng.normal(size=(E, H, I)) * 60)
+    q1[:, :I, 0] = S.round_e4m3(448.0)
+    q1[:, I:, 0] = S.round_e4m3(rng.uniform(64, 448, (E, I)) * rng.choice([-1, 1], (E, I)))
+    s1, s2 = np.empty((E, 2, 1), np.float32), np.full((E, 1, 1), 2.0 ** -8, np.float32)
+    s1[:, 0, 0] = np.array(gs) / 448
+    s1[:, 1, 0] = 2.0 ** np.clip(np.round(-np.minimum(gs, 0) / np.log(2)) - 7, 0, 118)  # h up to about 100
+    ex = ScaledExperts(gpu(q1), gpu(s1), gpu(q2), gpu(s2), max_tokens=T, k=1)
+    x = torch.zeros(T, H, device="cuda")
+    x[:, 0] = 1.0
+    idx = (np.arange(T) % E).astype(np.int32)[:, None]
+    y = ex.forward(x, gpu(idx), torch.ones(T, 1, device="cuda")).double().cpu().numpy()
+    assert B.pw_get_status() == B.PW_OK
+    for e in range(E):
+        g, u = float(np.float32(448.0 * float(s1[e, 0, 0]))), S.values(q1[e, I:, :1], s1[e, 1:], 128)[:, 0]
+        h = S.silu(g) * u
+        q, sc = S.quantize(h[None], 1)
+        hv, w2 = S.values(q, sc, 1)[0], S.values(q2[e], s2[e], 128)
+        top, a = np.abs(h).max(), np.abs(h) / sc[0, 0]
+        assert S.block_scale(top * (1 - 2.0 ** -15)) == S.block_scale(top * (1 + 2.0 ** -15))
+        step = np.maximum(2.0 ** (np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3), 2.0 ** -9)
+        near = np.abs(a / step - np.floor(a / step) - 0.5) * step <= 2.0 ** -15 * a
+        tol = np.abs(w2) @ np.where(near, step * sc[0, 0], 0) + sum_bound(1) * (np.abs(w2) @ (1.25 * np.abs(hv)))
+        ref = w2 @ hv
+        assert (np.abs(y[idx[:, 0] == e] - ref) <= tol).all(), gs[e]
+        assert g == 0 or np.abs(y[idx[:, 0] == e]).max() > 0, gs[e]
+
+
 def test_layer_bad_expert_is_recorded(libpw):
     import torch
     from any_precision_expert_pw_b200.scaled_layer import ScaledExperts

@@ -50,7 +50,9 @@ class ScaledExperts:
     gate_up uint8 [E][2I][H] and down uint8 [E][H][I] e4m3 bytes, their fp32 scales
     [E][2I/128][H/128] and [E][H/128][I/128] (quantize_weights gives both), kept by reference.
     max_tokens x k assignments at most in one call.  Calls on different streams that may overlap
-    need an object each (they would share the workspace)."""
+    need an object each (they would share the workspace); a stream other than the one current at
+    construction has to be ordered behind it.  Streams given to forward have to exist as long as
+    this object, and the object as long as a graph that captured its calls."""
 
     def __init__(self, gate_up, gate_up_scale, down, down_scale, max_tokens: int, k: int):
         torch = _torch()
@@ -75,6 +77,7 @@ class ScaledExperts:
         if not self.ws_bytes:
             raise B.PwError(B.PW_ERR_INVALID_ARG, "pw_moe_scaled_workspace_bytes")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._streams = set()  # streams that the workspace and the weights are recorded on
         self._ws_ptr = self.workspace.data_ptr()
         self.experts = B.pw_scaled_experts(E=E, H=H, I=I, gate_up=gate_up.data_ptr(),
                                            gate_up_scale=gate_up_scale.data_ptr(),
@@ -82,11 +85,22 @@ class ScaledExperts:
 
     def forward(self, x, idx, gate, y=None, stream=None):
         """y[t] = sum over s of gate[t][s] * FFN(expert idx[t][s], x[t]); idx -1 = empty slot.
-        x, y [T][H] float32, bfloat16 or float16, idx int32 [T][k], gate float32 [T][k]."""
+        x, y [T][H] float32, bfloat16 or float16, idx int32 [T][k], gate float32 [T][k], T >= 1.
+        stream: handle of the stream to run on (the current one if None).  It has to be ordered behind
+        what made the tensors; they may be freed while it still runs."""
         torch = _torch()
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.forward(x, idx, gate, y, stream)
+        current = torch.cuda.current_stream()
+        s = current.cuda_stream if stream is None else stream
+        on = current if s == current.cuda_stream else torch.cuda.ExternalStream(s, self.device)
         T = x.shape[0]
-        if y is None:
+        if y is None and on is current:
             y = torch.empty_like(x)
+        elif y is None:
+            with torch.cuda.stream(on):
+                y = torch.empty_like(x)
         if x.shape != (T, self.H) or y.shape != (T, self.H):
             raise ValueError(f"x {tuple(x.shape)}, y {tuple(y.shape)}: [T][{self.H}] expected")
         if idx.shape != (T, self.k) or gate.shape != (T, self.k) or T > self.max_tokens:
@@ -97,10 +111,15 @@ class ScaledExperts:
         for t in (x, idx, gate, y):
             if t.device != self.device or not t.is_contiguous():
                 raise ValueError("contiguous tensors on the experts' device expected")
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                return self.forward(x, idx, gate, y, stream)
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        # memory that the allocator may not hand out again before this stream is done with it
+        if s not in self._streams:
+            for t in (self.workspace, *self._keep):
+                t.record_stream(on)
+            self._streams.add(s)
+        if on is not current:
+            for t in (x, idx, gate, y):
+                t.record_stream(on)
+            y.record_stream(current)
         B.check(B.pw_moe_scaled_forward(self.experts, x.data_ptr(), type_of(x), T, self.k,
                                         idx.data_ptr(), gate.data_ptr(), y.data_ptr(), type_of(y),
                                         self._ws_ptr, self.ws_bytes, s), "pw_moe_scaled_forward")

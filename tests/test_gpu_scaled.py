@@ -435,6 +435,53 @@ def test_layer_two_streams_with_their_own_workspaces(libpw):
     assert B.pw_get_status() == B.PW_OK
 
 
+def test_layer_on_another_stream_keeps_its_memory(libpw):
+    """Tensors that a call on another stream uses may be dropped while it waits there: their memory is
+    not handed out again before that stream is done, and the call's own output belongs to both streams."""
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    H, I, E, T, k = 640, 384, 4, 50, 2
+    tensors, _, _ = _layer(H, I, E, 31)
+    x, idx, gate = torch.randn(T, H, device="cuda"), gpu(routing(T, E, k, 32)), torch.rand(T, k, device="cuda")
+    want = ScaledExperts(*tensors, max_tokens=T, k=k).forward(x, idx, gate) + 0   # every kernel loaded
+    torch.cuda.synchronize()
+
+    def fresh():
+        return [t.clone() for t in (*tensors, x, idx, gate)]
+
+    s, done = torch.cuda.Stream(), torch.cuda.Event()
+    mine = fresh()
+    ex = ScaledExperts(*mine[:4], max_tokens=T, k=k)
+    ex.workspace.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)                     # about 0.2 s
+    y = ex.forward(*mine[4:], stream=s.cuda_stream)
+    done.record(s)
+    sizes = [t.numel() * t.element_size() for t in (*mine, ex.workspace)]
+    held = [(t.data_ptr(), n) for t, n in zip((*mine, ex.workspace), sizes)]
+    del mine, ex
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    assert not done.query()                                # the call has not run yet
+    for t in again:
+        assert all(t.data_ptr() + t.numel() <= p or p + n <= t.data_ptr() for p, n in held)
+        t.fill_(0xFF)
+    torch.cuda.current_stream().wait_event(done)
+    assert bool((y == want).all())
+    # the output: dropped while the current stream still reads it, it is not given to the other stream
+    torch.cuda._sleep(400_000_000)
+    z, at, n = y + 0, y.data_ptr(), y.numel() * 4
+    done.record()
+    del y
+    with torch.cuda.stream(s):
+        other = torch.empty(n, dtype=torch.uint8, device="cuda")
+        assert not done.query()
+        assert other.data_ptr() + n <= at or at + n <= other.data_ptr()
+        other.fill_(0xFF)
+    torch.cuda.synchronize()
+    assert bool((z == want).all()) and B.pw_get_status() == B.PW_OK
+
+
 def test_quantized_weights_object(libpw):
     """quantize_weights: 128 x 128 blocks of each matrix, odd sizes included, and a layer on them
     close to the unquantised one (both roundings are at most 2^-4 of a value)."""

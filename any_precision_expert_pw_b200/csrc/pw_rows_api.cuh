@@ -282,7 +282,7 @@ pw_status launch_combine_grad(const void* dy, const void* o, int T, int k, int H
 
 // Workspace of pw_moe_scaled_forward.
 struct ScaledWorkspace {
-  size_t pos, src, offsets, sort, counter, xq, xs, hq, hs, o, part[2], total;
+  size_t pos, src, offsets, sort, counter, xq, xs, hq, hs, o, part, total;
 };
 ScaledWorkspace scaled_ws(int T, int k, int E, int H, int I) {
   ScaledWorkspace w;
@@ -297,15 +297,14 @@ ScaledWorkspace scaled_ws(int T, int k, int E, int H, int I) {
   w.pos = take(4 * n);
   w.src = take(4 * n);
   w.sort = take(pw_expert_sort_workspace_bytes(T, k, E));
-  w.counter = take(4 * 2 * kScaledMaxGrid);  // one set for each product
+  w.counter = take(4 * 2 * kScaledMaxGrid);  // one set for each product, both zeroed by the sort
   w.xq = take(n * H);
   w.xs = take(4 * n * (H / 128));
   w.hq = take(n * I);
   w.hs = take(4 * n * (I / 128));
   w.o = take(4 * n * H);
-  // one set of partials for each product: the second starts while the first still joins
-  w.part[0] = take(part_bytes(static_cast<int>(n)));
-  w.part[1] = take(part_bytes(static_cast<int>(n)));
+  // partials of either product: the second writes its own only when the first has ended
+  w.part = take(part_bytes(static_cast<int>(n)));
   w.total = at;
   return w;
 }
@@ -531,7 +530,7 @@ pw_status pw_moe_scaled_forward(const pw_scaled_experts* ex, const void* x, int 
   c.hs = hs;
   c.I = I;
   c.counter = counter;
-  c.part = reinterpret_cast<float*>(base + w.part[0]);
+  c.part = reinterpret_cast<float*>(base + w.part);
   s = launch_scaled(c, di->sms, st);
   if (s != PW_OK) return s;
   ScaledCall d = {};
@@ -550,7 +549,7 @@ pw_status pw_moe_scaled_forward(const pw_scaled_experts* ex, const void* x, int 
   d.y_type = PW_TYPE_F32;
   d.ld_y = H;
   d.counter = counter + kScaledMaxGrid;
-  d.part = reinterpret_cast<float*>(base + w.part[1]);
+  d.part = c.part;
   s = launch_scaled(d, di->sms, st);
   if (s != PW_OK) return s;
   return launch_combine(o, PW_TYPE_F32, T, k, H, H, pos, gate, y, y_type, H, st);

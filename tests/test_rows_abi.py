@@ -106,6 +106,17 @@ def test_layer_refusals(libpw):
     _bad(B.pw_moe_scaled_forward, good, changes)
 
 
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 8, 4096, 14336), (64, 8, 64, 3584, 2560), (4096, 8, 64, 3584, 2560)])
+def test_layer_workspace_holds_what_is_used(libpw, T, k, E, H, I):
+    """Positions, quantised rows and hidden rows with their scales, fp32 expert outputs, one set of
+    partials (up to 160 CTAs x 256 columns x 128 rows), counters and the sort's table: nothing twice."""
+    n = T * k
+    partials = 4 * 160 * 256 * min(128, -(-n // 32) * 32)
+    rows = n * (H + H // 32 + I + I // 32 + 4 * H)
+    small = 8 * n + 4 * (E + 1) + 8 * 160 + B.pw_expert_sort_workspace_bytes(T, k, E)
+    assert B.pw_moe_scaled_workspace_bytes(T, k, E, H, I) <= rows + partials + small + 12 * 256
+
+
 def test_experts_object_refuses_other_tensors():
     torch = pytest.importorskip("torch")
     from any_precision_expert_pw_b200.scaled_layer import ScaledExperts, type_of

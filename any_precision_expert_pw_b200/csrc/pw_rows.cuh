@@ -234,7 +234,7 @@ __device__ __forceinline__ int block_inclusive(int v, int* warp_sum) {
   return v + (warp ? warp_sum[warp - 1] : 0);
 }
 
-// part: counts of every CTA's run (NULL with one CTA).  zero: words set to zero (n_zero of them).
+// part: counts of every CTA's run (NULL with one CTA).  src may be NULL.  zero: n_zero words set to zero.
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t* idx, int n, int E,
                                                                   const int32_t* part, int32_t* pos,
                                                                   int32_t* src, int32_t* offsets,
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
       if (i < wb) {
         const int row = live ? base[x] + first + __popc(lower) : -1;
         pos[i] = row;
-        if (live) src[row] = i;
+        if (live && src) src[row] = i;
       }
     }
   }

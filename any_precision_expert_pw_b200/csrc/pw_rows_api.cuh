@@ -282,7 +282,7 @@ pw_status launch_combine_grad(const void* dy, const void* o, int T, int k, int H
 
 // Workspace of pw_moe_scaled_forward.
 struct ScaledWorkspace {
-  size_t pos, src, offsets, sort, counter, xq, xs, hq, hs, o, part, total;
+  size_t pos, offsets, sort, counter, xq, xs, hq, hs, o, part, total;
 };
 ScaledWorkspace scaled_ws(int T, int k, int E, int H, int I) {
   ScaledWorkspace w;
@@ -295,7 +295,6 @@ ScaledWorkspace scaled_ws(int T, int k, int E, int H, int I) {
   };
   w.offsets = take(4 * static_cast<size_t>(E + 1));
   w.pos = take(4 * n);
-  w.src = take(4 * n);
   w.sort = take(pw_expert_sort_workspace_bytes(T, k, E));
   w.counter = take(4 * 2 * kScaledMaxGrid);  // one set for each product, both zeroed by the sort
   w.xq = take(n * H);
@@ -508,9 +507,8 @@ pw_status pw_moe_scaled_forward(const pw_scaled_experts* ex, const void* x, int 
   float* hs = reinterpret_cast<float*>(base + w.hs);
   float* o = reinterpret_cast<float*>(base + w.o);
   cudaStream_t st = as_cuda(stream);
-  pw_status s = launch_sort(idx, T, k, E, pos, reinterpret_cast<int32_t*>(base + w.src), offsets,
-                            reinterpret_cast<int32_t*>(base + w.sort), counter, 2 * kScaledMaxGrid,
-                            di->sms, st);
+  pw_status s = launch_sort(idx, T, k, E, pos, nullptr, offsets, reinterpret_cast<int32_t*>(base + w.sort),
+                            counter, 2 * kScaledMaxGrid, di->sms, st);
   if (s != PW_OK) return s;
   s = launch_quantize_rows(x, x_type, T, H, H, k, pos, xq, H, xs, st);
   if (s != PW_OK) return s;

@@ -113,7 +113,7 @@ def test_layer_workspace_holds_what_is_used(libpw, T, k, E, H, I):
     n = T * k
     partials = 4 * 160 * 256 * min(128, -(-n // 32) * 32)
     rows = n * (H + H // 32 + I + I // 32 + 4 * H)
-    small = 8 * n + 4 * (E + 1) + 8 * 160 + B.pw_expert_sort_workspace_bytes(T, k, E)
+    small = 4 * n + 4 * (E + 1) + 8 * 160 + B.pw_expert_sort_workspace_bytes(T, k, E)
     assert B.pw_moe_scaled_workspace_bytes(T, k, E, H, I) <= rows + partials + small + 12 * 256
 
 

@@ -22,40 +22,8 @@ struct ElemSize {
   static constexpr int value = TY == PW_TYPE_F32 ? 4 : 2;
 };
 
-// V consecutive elements at p as fp32: V = 1, or the 16 bytes of a vector (aligned).
-template <int TY, int V>
-__device__ __forceinline__ void load_elems(const void* p, float (&v)[V]) {
-  if constexpr (TY == PW_TYPE_F32) {
-    static_assert(V == 1 || V == 4 || V == 8, "vector");
-    if constexpr (V == 1) {
-      v[0] = __ldg(static_cast<const float*>(p));
-    } else {
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const float4 a = __ldg(static_cast<const float4*>(p) + i);
-        v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
-      }
-    }
-  } else {
-    static_assert(V == 1 || V == 8, "vector");
-    if constexpr (V == 1) {
-      const uint16_t b = __ldg(static_cast<const unsigned short*>(p));
-      v[0] = TY == PW_TYPE_BF16 ? bf16_to_f32(b) : f16_to_f32(b);
-    } else {
-      const uint4 a = __ldg(static_cast<const uint4*>(p));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint16_t lo = static_cast<uint16_t>(w[i]), hi = static_cast<uint16_t>(w[i] >> 16);
-        v[2 * i] = TY == PW_TYPE_BF16 ? bf16_to_f32(lo) : f16_to_f32(lo);
-        v[2 * i + 1] = TY == PW_TYPE_BF16 ? bf16_to_f32(hi) : f16_to_f32(hi);
-      }
-    }
-  }
-}
-
-// The same V elements as they lie in memory (half the registers of fp32 for 16-bit types: what bounds
-// the row kernels is loads in flight), and their values.
+// V consecutive elements at p as they lie in memory (one load; half the registers of fp32 for 16-bit
+// types: what bounds the row kernels is loads in flight), and their values.
 template <int TY, int V>
 struct Raw {
   uint32_t w[V * ElemSize<TY>::value / 4 > 0 ? V * ElemSize<TY>::value / 4 : 1];
@@ -449,7 +417,7 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(
     const bool in = static_cast<int>(threadIdx.x) < k;
     const long long slot = static_cast<long long>(t) * k + threadIdx.x;
     s_row[threadIdx.x] = in ? checked_row(pos, slot, T * k) : -1;
-    s_gate[threadIdx.x] = in ? (gate ? gate[slot] : 1.0f) : 0.0f;
+    s_gate[threadIdx.x] = in ? gate[slot] : 0.0f;
   }
   __syncthreads();
   float acc[KM];
@@ -678,9 +646,9 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const void* x, lon
   float m = 0.0f;
   if (c < cols)
     for (int r = half; r < nr; r += 2) {
-      float v[1];
-      load_elems<TY, 1>(elem_at(x, static_cast<size_t>(r0 + r) * ld_x + c, S), v);
-      m = fmaxf(m, finite_abs(v[0]));
+      Raw<TY, 1> v;
+      load_raw<TY, 1>(elem_at(x, static_cast<size_t>(r0 + r) * ld_x + c, S), v);
+      m = fmaxf(m, finite_abs(raw_value<TY, 1>(v, 0)));
     }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -694,9 +662,10 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const void* x, lon
   if (threadIdx.x == 0) scale[rb * blocks + b] = pow2(e);
   if (c < cols)
     for (int r = half; r < nr; r += 2) {
-      float v[1];
-      load_elems<TY, 1>(elem_at(x, static_cast<size_t>(r0 + r) * ld_x + c, S), v);
-      q[static_cast<size_t>(r0 + r) * ld_q + c] = static_cast<uint8_t>(e4m3_pair(v[0] * inv, 0.0f) & 0xffu);
+      Raw<TY, 1> v;
+      load_raw<TY, 1>(elem_at(x, static_cast<size_t>(r0 + r) * ld_x + c, S), v);
+      q[static_cast<size_t>(r0 + r) * ld_q + c] =
+          static_cast<uint8_t>(e4m3_pair(raw_value<TY, 1>(v, 0) * inv, 0.0f) & 0xffu);
     }
 }
 

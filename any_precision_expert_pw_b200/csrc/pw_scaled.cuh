@@ -93,7 +93,7 @@ struct alignas(64) Params {
 
 // ---- schedule (the same in every role) ----
 struct Sched {
-  int units, waves, rem, pieces, run;  // run: K blocks of the remainder, cut into `pieces`
+  int waves, rem, pieces, run;  // run: K blocks of the remainder, cut into `pieces`
 };
 // The units behind the last whole wave are cut while CTAs would stay without one: every such unit
 // into the same number of pieces, so that a unit has the fewest pieces to join.  (Cutting them into
@@ -101,7 +101,6 @@ struct Sched {
 // 28672 x 4096, 112 units, 34.6 us against 29.0 with 112 CTAs at work; 112 SMs draw what HBM gives.)
 __device__ __forceinline__ Sched make_sched(int units, int kb, int grid, int min_piece) {
   Sched s;
-  s.units = units;
   s.waves = units / grid;
   s.rem = units - s.waves * grid;
   s.run = s.rem * kb;

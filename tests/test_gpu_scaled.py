@@ -318,6 +318,56 @@ def test_layer(libpw, T, k, E, H, I, xt, yt):
     assert float(np.median(tol)) < 0.05 * float(np.sqrt((ref ** 2).mean()))
 
 
+class OnDemand:
+    """The values of experts' weights on the device, one expert at a time."""
+
+    def __init__(self, q, s):
+        self.q, self.s, self.shape = q, s, tuple(q.shape)
+
+    def __getitem__(self, e):
+        return S.values(self.q[e].cpu().numpy(), self.s[e].cpu().numpy(), 128)
+
+
+def device_weights(E, N, K, gen):
+    import torch
+    q = torch.empty(E, N, K, dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        v = torch.randn(N, K, generator=gen, device="cuda").mul_(120).clamp_(-448, 448)
+        q[e] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+    return q, torch.exp(torch.randn(E, N // 128, K // 128, generator=gen, device="cuda") * 0.3 - 7)
+
+
+# the layers' own sizes: one token, a decode batch (both on the few-rows kernel), a prompt (large-rows)
+@pytest.mark.parametrize("T,k,E,H,I,pick", [(1, 2, 8, 4096, 14336, [0]), (64, 8, 64, 3584, 2560, [0, 40]),
+                                            (400, 8, 64, 3584, 2560, [3, 200, 396])])
+def test_layer_at_its_real_sizes(libpw, T, k, E, H, I, pick):
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    q1, s1 = device_weights(E, 2 * I, H, gen)
+    q2, s2 = device_weights(E, H, I, gen)
+    ex = ScaledExperts(q1, s1, q2, s2, max_tokens=T, k=k)
+    ex.workspace.fill_(0xFF)
+    idx, gate = routing(T, E, k, 33), torch.rand(T, k, generator=gen, device="cuda")
+    if T > 100:
+        idx[T - 3:] = -1                                   # a padded batch
+    x = torch.randn(T, H, generator=gen, device="cuda").bfloat16()
+    y = ex.forward(x, gpu(idx), gate, torch.empty(T, H, device="cuda"))
+    again = ex.forward(x, gpu(idx), gate, torch.empty(T, H, device="cuda"))
+    assert B.pw_get_status() == B.PW_OK and bool((y == again).all())
+    ref, tol = moe_bound(x[pick].double().cpu().numpy(), idx[pick], gate[pick].cpu().numpy(), OnDemand(q1, s1),
+                         OnDemand(q2, s2))
+    tol = tol + U * (np.abs(ref) + tol)
+    got = y[pick].double().cpu().numpy()
+    assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) / tol))
+    # granting each of K terms its rounding moves many h to a border: the bound is 0.25 to 0.35 of the
+    # outputs' rms here, and a wrong expert, gate or block moves thousands of outputs by more
+    assert float(np.median(tol)) < 0.5 * float(np.sqrt((ref ** 2).mean()))
+    if T > 100:
+        assert bool((y[T - 3:] == 0).all())
+
+
 @pytest.mark.parametrize("n", [2, 40])                     # tokens an expert: both kernels
 def test_layer_of_very_negative_gates(libpw, n):
     """SiLU(g) u where e^-g passes 2^126 and 2^128 and u makes up for it.  x has one value, so g and u are

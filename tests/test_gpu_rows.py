@@ -340,3 +340,47 @@ def test_run_together_in_a_graph_on_another_stream(libpw):
         mag = (np.abs(X * D)).sum(1, keepdims=True)
         assert (np.abs(dg.cpu().numpy() - dots) <= (H / 256 + 21) * U * mag).all()
     assert B.pw_get_status() == B.PW_OK
+
+
+@pytest.mark.parametrize("T,k,H,name", [(1 << 20, 16, 24, "bf16"), (1 << 24, 1, 3, "f16"), (2, 3, 1 << 18, "f32"),
+                                        (3, 2, (1 << 18) - 1, "bf16")])
+def test_movement_of_largest_sizes(libpw, T, k, H, name):
+    """2^24 rows, and rows of 2^18 columns: small whole numbers, so that every sum is exact in fp32."""
+    import torch
+    E, ty, dt = 5, TYPES[name], _torch_type(name)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    idx = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    pos = torch.empty_like(idx)
+    src, off = torch.full((T * k,), -7, dtype=torch.int32, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    n = B.pw_expert_sort_workspace_bytes(T, k, E)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    B.check(B.pw_expert_sort(idx.data_ptr(), T, k, E, pos.data_ptr(), src.data_ptr(), off.data_ptr(),
+                             ws.data_ptr(), n))
+    live = int(off[-1])
+    x = torch.randint(-3, 4, (T, H), generator=g, device="cuda", dtype=torch.int8).to(dt)
+    gate = torch.randint(1, 3, (T, k), generator=g, device="cuda").float()
+    xs = torch.full((T * k, H), -77.0, dtype=dt, device="cuda")
+    B.check(B.pw_expert_dispatch(x.data_ptr(), ty, T, k, H, H, pos.data_ptr(), xs.data_ptr(), H))
+    token = src[:live].long() // k
+    for a in range(0, live, 1 << 22):
+        b = min(live, a + (1 << 22))
+        assert bool((xs[a:b] == x[token[a:b]]).all())
+    assert bool((xs[live:] == -77.0).all())
+    there = (pos >= 0).float()
+    y, d_x = torch.empty_like(x), torch.empty_like(x)
+    B.check(B.pw_expert_combine(xs.data_ptr(), ty, T, k, H, H, pos.data_ptr(), gate.data_ptr(), y.data_ptr(), ty, H))
+    B.check(B.pw_expert_dispatch_grad(xs.data_ptr(), ty, T, k, H, H, pos.data_ptr(), d_x.data_ptr(), H))
+    # whole numbers up to 16 * 2 * 3 = 96 are exact in every type
+    assert bool((y == ((gate * there).sum(1, keepdim=True) * x.float()).to(dt)).all())
+    assert bool((d_x == (there.sum(1, keepdim=True) * x.float()).to(dt)).all())
+    d_gate, d_o = torch.empty_like(gate), torch.full_like(xs, -77.0)
+    B.check(B.pw_expert_combine_grad(x.data_ptr(), xs.data_ptr(), ty, T, k, H, H, H, pos.data_ptr(), gate.data_ptr(),
+                                     d_o.data_ptr(), H, d_gate.data_ptr()))
+    # at most 9 * 2^18 < 2^24: exact
+    assert bool((d_gate == there * (x.float() ** 2).sum(1, keepdim=True)).all())
+    weight = gate.reshape(-1)[src[:live].long()]
+    for a in range(0, live, 1 << 22):
+        b = min(live, a + (1 << 22))
+        assert bool((d_o[a:b] == (weight[a:b, None] * xs[a:b].float()).to(dt)).all())
+    assert bool((d_o[live:] == -77.0).all()) and B.pw_get_status() == B.PW_OK

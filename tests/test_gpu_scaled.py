@@ -659,3 +659,47 @@ def test_wait_that_never_completes_times_out(libpw, M):
     xv = S.values(*S.quantize(x.double().cpu().numpy(), 1), 1)
     ref, mag = xv @ v[0].T, np.abs(xv) @ np.abs(v[0]).T
     assert (np.abs(y.double().cpu().numpy() - ref) <= (sum_bound(K // 128) + U) * mag).all()
+
+
+@pytest.mark.parametrize("M,N,K,pick", [(1 << 24, 40, 48, [0, 1, 5_000_001, (1 << 24) - 1]), (3, 130, 1 << 18, [0, 2]),
+                                        (70, 130, (1 << 18) - 3, [0, 69]), (2, 1 << 18, 136, [0, 1])])
+def test_products_of_largest_sizes(libpw, M, N, K, pick):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(N)
+    ld, kb = -(-K // 16) * 16, -(-K // 128)
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    xq, xs = torch.full((M, ld), 127, dtype=torch.uint8, device="cuda"), torch.empty(M, kb, device="cuda")
+    B.check(B.pw_scaled_quantize(x.data_ptr(), B.PW_TYPE_BF16, M, K, K, 1, xq.data_ptr(), ld, xs.data_ptr()))
+    q, s, v = weights(1, N, K, 34)
+    w, ldw = padded_codes(q)
+    ws, n = gpu(s), B.pw_scaled_gemm_workspace_bytes(M, N, K, 1)
+    tmp, y = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.full((M + 1, N), -7.0, device="cuda")
+    B.check(B.pw_scaled_gemm(xq.data_ptr(), xs.data_ptr(), M, K, ld, w.data_ptr(), ws.data_ptr(), 1, N, ldw, 0,
+                             y.data_ptr(), B.PW_TYPE_F32, N, tmp.data_ptr(), n))
+    assert B.pw_get_status() == B.PW_OK and bool((y[M] == -7.0).all())
+    xv = S.values(*S.quantize(x[pick].double().cpu().numpy(), 1), 1)
+    ref, mag = xv @ v[0].T, np.abs(xv) @ np.abs(v[0]).T
+    assert (np.abs(y[pick].double().cpu().numpy() - ref) <= (sum_bound(kb) + U) * mag).all()
+
+
+def test_layer_of_the_largest_batch(libpw):
+    """2^24 assignments: the rows of some tokens against the oracle, padding zero."""
+    import torch
+    from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
+    T, k, E, H, I = 1 << 21, 8, 16, 128, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(35)
+    tensors, v1, v2 = _layer(H, I, E, 36)
+    ex = ScaledExperts(*tensors, max_tokens=T, k=k)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, dim=1).indices.int()
+    idx[T - 1000:] = -1
+    gate = torch.rand(T, k, generator=g, device="cuda")
+    y = ex.forward(x, idx, gate, torch.empty(T, H, device="cuda"))
+    assert B.pw_get_status() == B.PW_OK and bool((y[T - 1000:] == 0).all()) and bool(y.isfinite().all())
+    pick = [0, 1, 77_777, T // 2, T - 1001]
+    ref, tol = moe_bound(x[pick].double().cpu().numpy(), idx[pick].cpu().numpy(), gate[pick].cpu().numpy(), v1, v2)
+    assert (np.abs(y[pick].double().cpu().numpy() - ref) <= tol + U * (np.abs(ref) + tol)).all()

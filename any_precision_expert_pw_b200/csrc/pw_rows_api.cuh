@@ -134,10 +134,15 @@ struct ScaledCall {
   int32_t* counter;
 };
 
-// Rows per expert (on average over the experts that can have one) up to which the few-rows kernel is
-// used: with 32 it is ahead (64 experts x 32 rows, 5120 x 3584: 194 us against 206; one matrix, 32 rows:
-// 16.7 against 20.6), with 64 even or behind (212 against 214; 64 x 28672 x 4096: 36 against 31), and
-// ragged groups of 50 rows on average, many above 64, take 96 against 80.
+// Rows per expert, on average over the experts that can have one, up to which the few-rows kernel is
+// used.  With even loads it is ahead up to there (64 experts of 8, 16 and 32 rows, 5120 x 3584: 180, 190 and
+// 198 us against 201, 206 and 213; one matrix, 32 rows: 16.7 against 20.6), with 64 even or behind (64 x
+// 28672 x 4096: 36 against 31), and ragged groups of 50 rows on average, many above 64, take 96 against 80.
+// The host does not know the loads: M counts empty slots, and rows on few of the experts (a remap to a
+// critical set, a skewed router) are more to each than this average.  What counts is the rows of an
+// expert in use: 2048 rows on 64, 32, 16 and 4 of 64 experts take 198, 144, 117 and 102 us here and 213, 133,
+// 80 and 58 with the large-rows kernel, 512 rows 180, 105, 68 and 41 against 201, 119, 73 and 25; loads
+// falling as 1 / rank, 2048 rows: 237 against 229, 512 rows: 189 against 217.
 constexpr int kFewRows = 32;
 
 int part_rows(int M) { return static_cast<int>(align_up(std::min(M, pw::k7::kTileM), 32)); }
@@ -235,8 +240,8 @@ pw_status launch_combine_types(const void* o, int T, int k, int H, long long ld_
   constexpr int VI = 16 / pw::ElemSize<TI>::value;  // elements of one 16-byte load
   const bool vec = vec_ok(o, pw::ElemSize<TI>::value, H, ld_o) && aligned(y, 16) &&
                    ld_y * pw::ElemSize<TO>::value % 16 == 0;
-    // vectors (single elements) of a lane; 16-bit types take one of 8 (8192 x 8 rows of 3584 bf16: 41.6
-  // us, two 44.3), fp32 two of 4 (53.9 us, one 57.6)
+  // vectors (single elements) of a lane; 16-bit types take one of 8 (4096 x 8 rows of 3584 bf16: 41.6
+  // us, two 44.3), fp32 two of 4 (8192 x 4 rows of 2048: 53.9 us, one 57.6)
   constexpr int UV = 8 / VI, US = 8;
   const int cols = vec ? 32 * UV * VI : 32 * US;  // columns of one warp
   const int groups = (H + cols - 1) / cols;

@@ -11,16 +11,19 @@
 //
 // Work: units of 128 rows x 256 columns (gated: 128 gate and the 128 matching up columns), in order
 // of expert, column tile, row tile; one CTA per SM.  Whole waves of units go one unit to a CTA.  Where
-// the rest (U mod SMs units) would leave CTAs idle each of its units is cut along K into pieces, one
-// per CTA, and joined by the CTA that finishes last (partials and a counter in the workspace; the sum
-// runs in piece order whoever joins, so results repeat bit for bit).  Nobody waits for another CTA.
+// the rest (U mod SMs units) is at most half the grid, each of its units is cut along K into as many
+// pieces as there are CTAs for it (none shorter than kMinPiece blocks) and joined by the CTA that
+// finishes last (partials and a counter in the workspace; the sum runs in piece order whoever joins, so
+// results repeat bit for bit); a larger rest stays whole and the CTAs behind it idle.  Nobody waits
+// for another CTA.
 //
 // What bounds it: per SM and block the products take 512 cycles, and two blocks (2 x 256 columns) are
-// all that tensor memory holds, so a block's turn is half of products + signals + reading back:
-// about 875 cycles (4736 x 1024, one unit an SM: 0.55 us a block at the 1.6 GHz seen under this load,
-// 2.0 PFLOP/s; 4096 x 5120 x 3584: 88 us, 1.7 PFLOP/s).  Tried and slower: 128-column products
-// with four half stages (rows read twice from shared memory), sixteen epilogue warps of 64
-// columns, scales loaded two blocks ahead (registers).
+// all that tensor memory holds, so a block's turn is half of products + signals + reading back.  4736 x
+// 1024 x 16384, one unit of 128 blocks an SM: 84 us alone and 141,000 cycles at 1.68 GHz, so 1,100 a block
+// with the launch's start and end, the tensor pipe 50 % active; 80 us a launch back to back (2.0
+// PFLOP/s).  4096 x 5120 x 3584, 126 blocks on the fullest SM: 98 us alone, 86 back to back (1.75 PFLOP/s).
+// Tried and slower: 128-column products with four half stages (rows read twice from shared memory),
+// sixteen epilogue warps of 64 columns, scales loaded two blocks ahead (registers).
 //
 // Order of launches: a launch before the one in front of this one has completed when this one starts
 // (every kernel here lets its dependents start only after its own wait), so the offsets and the
@@ -95,7 +98,7 @@ struct alignas(64) Params {
 struct Sched {
   int waves, rem, pieces, run;  // run: K blocks of the remainder, cut into `pieces`
 };
-// The units behind the last whole wave are cut while CTAs would stay without one: every such unit
+// The units behind the last whole wave are cut where each can have two CTAs or more: every such unit
 // into the same number of pieces, so that a unit has the fewest pieces to join.  (Cutting them into
 // equal runs for all CTAs, wherever a unit ends, costs more in joins than it spreads: 4 tokens x
 // 28672 x 4096, 112 units, 34.6 us against 29.0 with 112 CTAs at work; 112 SMs draw what HBM gives.)
@@ -181,8 +184,8 @@ __device__ __forceinline__ Unit find_unit(const Params& p, const int* tiles, con
 // ---- waits ----
 // Bounded wait on an mbarrier, as mbar_wait, but the clock and the limit (a global load) are read
 // only after several suspended tries: this kernel hands tensor-memory stages back and forth every
-// few hundred cycles, and a wait that reads the limit first costs more than a stage takes (4736 x
-// 1024 x 16384: 98.9 us with mbar_wait, 88.8 us so).
+// few hundred cycles, and reading the limit first lengthens every wait (4736 x 1024 x 16384, back to back:
+// 83.3 us with mbar_wait, 81.7 us so).
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const unsigned long long t0 = global_ns();
   const unsigned long long limit = wait_limit_ns();

@@ -1,7 +1,7 @@
 """Expert FFN on e4m3 weights (libpw's pw_moe_scaled_forward) with torch tensors as the buffers.
 
 Beside ``device_layer.DeviceLayer`` (any-precision experts): the same layer on experts held in 8-bit
-floating point with one scale per 128 x 128 block, for batches of any length.  PyTorch allocates
+floating point with one scale per 128 x 128 block, for batches of up to 2^24 assignments.  PyTorch allocates
 device memory and names the stream; quantisation, sorting, both products and the combine run in
 libpw's kernels.  Routing comes from ``pw_route_topk`` and the rewrites (``DeviceLayer.route``).
 """

@@ -436,10 +436,11 @@ pw_status pw_plan_bitwidths(int nblocks, const double* damage, const uint64_t* b
 /* =======================================================================================
  * Token rows sorted by expert and back, and products in 8-bit floating point.
  *
- * The calls below take batches of any length (a prompt, a training batch) and the routing that
- * pw_route_topk and the rewrites give.  idx[t][s] = -1 is an empty slot (a padded token, a
+ * The calls below take batches of up to PW_MAX_ROWS slots (a prompt, a training batch; at least
+ * one token) and the routing that pw_route_topk and the rewrites give, for batches above
+ * PW_MAX_TOKENS in chunks of those calls.  idx[t][s] = -1 is an empty slot (a padded token, a
  * dropped assignment): it has no row, adds nothing to a sum and gets a zero gradient.  Rows
- * behind the last one in use (offsets[E]) are neither read nor written.
+ * behind the last one in use (offsets[E]) have no influence and are not written.
  * Row strides are in elements.  Sums are fp32 and each output is rounded once, to nearest even.
  * Every sum has a fixed order: results repeat bit for bit.
  * Row pointers are aligned to their elements; 16-byte aligned rows of whole 16-byte vectors are
@@ -461,7 +462,7 @@ enum { PW_TYPE_F32 = 0, PW_TYPE_BF16 = 1, PW_TYPE_F16 = 2 };
  *   offsets[e] .. offsets[e+1] - 1.
  *   1 <= k <= PW_MAX_TOPK, 1 <= T * k <= PW_MAX_ROWS, 1 <= E <= PW_MAX_EXPERTS.
  *   workspace: >= pw_expert_sort_workspace_bytes(T, k, E) bytes (0 on bad sizes), 256-byte
- *   aligned, contents need no initialisation.
+ *   aligned, contents need no initialisation; calls that may overlap need one each.
  * ------------------------------------------------------------------------------------- */
 size_t pw_expert_sort_workspace_bytes(int T, int k, int E);
 pw_status pw_expert_sort(const int32_t* idx, int T, int k, int E, int32_t* pos, int32_t* src,

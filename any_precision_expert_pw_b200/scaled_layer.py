@@ -87,20 +87,22 @@ class ScaledExperts:
         """y[t] = sum over s of gate[t][s] * FFN(expert idx[t][s], x[t]); idx -1 = empty slot.
         x, y [T][H] float32, bfloat16 or float16, idx int32 [T][k], gate float32 [T][k], T >= 1.
         stream: handle of the stream to run on (the current one if None).  It has to be ordered behind
-        what made the tensors; they may be freed while it still runs."""
+        what made the tensors.  The experts and the workspace may be dropped while it still runs, and a
+        y that is made here is safe on both streams; given tensors stay with the caller, who keeps them
+        or records the stream on them (Tensor.record_stream) if they are another stream's."""
         torch = _torch()
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 return self.forward(x, idx, gate, y, stream)
-        current = torch.cuda.current_stream()
-        s = current.cuda_stream if stream is None else stream
-        on = current if s == current.cuda_stream else torch.cuda.ExternalStream(s, self.device)
-        T = x.shape[0]
-        if y is None and on is current:
-            y = torch.empty_like(x)
-        elif y is None:
-            with torch.cuda.stream(on):
+        if stream is None:
+            stream = torch.cuda.current_stream().cuda_stream
+            if y is None:
                 y = torch.empty_like(x)
+        elif y is None:  # of the stream that writes it, known to the one that will read it
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device)):
+                y = torch.empty_like(x)
+            y.record_stream(torch.cuda.current_stream())
+        T = x.shape[0]
         if x.shape != (T, self.H) or y.shape != (T, self.H):
             raise ValueError(f"x {tuple(x.shape)}, y {tuple(y.shape)}: [T][{self.H}] expected")
         if idx.shape != (T, self.k) or gate.shape != (T, self.k) or T > self.max_tokens:
@@ -111,16 +113,12 @@ class ScaledExperts:
         for t in (x, idx, gate, y):
             if t.device != self.device or not t.is_contiguous():
                 raise ValueError("contiguous tensors on the experts' device expected")
-        # memory that the allocator may not hand out again before this stream is done with it
-        if s not in self._streams:
+        if stream not in self._streams:  # the allocator keeps this memory until that stream is done with it
+            on = torch.cuda.ExternalStream(stream, self.device)
             for t in (self.workspace, *self._keep):
                 t.record_stream(on)
-            self._streams.add(s)
-        if on is not current:
-            for t in (x, idx, gate, y):
-                t.record_stream(on)
-            y.record_stream(current)
+            self._streams.add(stream)
         B.check(B.pw_moe_scaled_forward(self.experts, x.data_ptr(), type_of(x), T, self.k,
                                         idx.data_ptr(), gate.data_ptr(), y.data_ptr(), type_of(y),
-                                        self._ws_ptr, self.ws_bytes, s), "pw_moe_scaled_forward")
+                                        self._ws_ptr, self.ws_bytes, stream), "pw_moe_scaled_forward")
         return y

@@ -486,8 +486,9 @@ def test_layer_two_streams_with_their_own_workspaces(libpw):
 
 
 def test_layer_on_another_stream_keeps_its_memory(libpw):
-    """Tensors that a call on another stream uses may be dropped while it waits there: their memory is
-    not handed out again before that stream is done, and the call's own output belongs to both streams."""
+    """Experts and workspace may be dropped while a call on another stream waits there: their memory is
+    not handed out again before that stream is done, and the call's own output belongs to both streams.
+    (Given activations are the caller's to record.)"""
     import torch
     from any_precision_expert_pw_b200.scaled_layer import ScaledExperts
     H, I, E, T, k = 640, 384, 4, 50, 2
@@ -507,6 +508,8 @@ def test_layer_on_another_stream_keeps_its_memory(libpw):
     with torch.cuda.stream(s):
         torch.cuda._sleep(400_000_000)                     # about 0.2 s
     y = ex.forward(*mine[4:], stream=s.cuda_stream)
+    for t in mine[4:]:
+        t.record_stream(s)
     done.record(s)
     sizes = [t.numel() * t.element_size() for t in (*mine, ex.workspace)]
     held = [(t.data_ptr(), n) for t, n in zip((*mine, ex.workspace), sizes)]
